@@ -23,8 +23,10 @@ MA_BF16 = 1
 MA_EQ_OFF, MA_EQ_ROWS_PRE, MA_EQ_ROWS_POST, MA_EQ_ROWS_RMS = 0, 1, 2, 3
 MA_SCALE_NONE, MA_SCALE_SQRT_MAX1_R_OVER_C, MA_SCALE_MOONSHOT, MA_SCALE_SQRT_MAX = 0, 1, 2, 3
 MA_MAX_NS_STEPS = 16
-KERNEL_KINDS = ("rownorm", "finalize", "pre", "gram", "poly", "axpy", "post", "adamw", "lion", "axpy_update")
+KERNEL_KINDS = ("rownorm", "finalize", "pre", "gram", "poly", "axpy", "post", "adamw", "lion", "axpy_update",
+                "embedding", "layernorm", "act", "weight_grad")
 MA_WORKSPACE_ALIGN = 256
+MA_ACT_BLOCK = 128
 MA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -84,6 +86,22 @@ EXPORTS = {
                                      C.c_size_t, C.POINTER(AdamWSegmentC), C.c_int32, C.c_int32, C.c_void_p,
                                      C.c_void_p]),
     "ma_lion_step": (C.c_int, [C.POINTER(LionSegmentC), C.c_int32, C.c_void_p]),
+    "ma_embedding_forward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_void_p, C.c_int32, C.c_int64,
+                                       C.c_float, C.c_void_p, C.c_int32, C.c_void_p]),
+    "ma_embedding_workspace_size": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64]),
+    "ma_embedding_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                                        C.c_float, C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "ma_layernorm_forward": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_float,
+                                       C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "ma_layernorm_workspace_size": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "ma_layernorm_backward": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_int64,
+                                        C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p,
+                                        C.c_void_p, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "ma_act_pack": (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "ma_act_unpack": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int32, C.c_void_p]),
+    "ma_act_weight_grad_workspace_size": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int32]),
+    "ma_act_weight_grad": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                                     C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
     "ma_status_string": (C.c_char_p, [C.c_int]),
     "ma_last_error": (C.c_char_p, []),
     "ma_version": (C.c_char_p, []),

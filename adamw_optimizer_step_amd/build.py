@@ -103,8 +103,8 @@ def _compile(src: str):
     return obj, res
 
 
-# Host-side sanitizers for the planner and argument validation (api.hip, the
-# host code of the C ABI): each flag applies to the host compilation only, so
+# Host-side sanitizers for the planner and argument validation (api.hip and
+# api_ops.hip, the host code of the C ABI): each flag applies to the host compilation only, so
 # the device code is the same as in the product library. The result is a
 # separate library for CPU-only tests, loaded with the ASan runtime preloaded.
 HOST_SANITIZE = ["-Xarch_host -fsanitize=address", "-Xarch_host -fsanitize=undefined",
@@ -113,7 +113,7 @@ SAN_LIB = os.path.join(BUILD, "host_sanitized", "libmuon_adamw_hostsan.so")
 
 
 def build_host_sanitized(verbose: bool = True) -> str:
-    """``libmuon_adamw_hostsan.so``: the library with api.hip's host code built
+    """``libmuon_adamw_hostsan.so``: the library with the C ABI's host code built
     under AddressSanitizer and UndefinedBehaviorSanitizer (for CPU tests of the
     ABI; run it with the ASan runtime preloaded, see ``asan_runtime``)."""
     out = os.path.dirname(SAN_LIB)
@@ -121,8 +121,8 @@ def build_host_sanitized(verbose: bool = True) -> str:
     sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     objs = []
     for src in sources:
-        if os.path.basename(src) == "api.hip":
-            obj = os.path.join(out, "api.hip.o")
+        if os.path.basename(src) in ("api.hip", "api_ops.hip"):
+            obj = os.path.join(out, os.path.basename(src) + ".o")
             flags = FLAGS + [f for pair in HOST_SANITIZE for f in pair.split()]
             r = subprocess.run([HIPCC, *flags, "-c", src, "-o", obj], capture_output=True, text=True)
             if r.returncode != 0:

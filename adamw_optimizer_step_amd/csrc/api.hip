@@ -19,14 +19,16 @@
 #include "adamw.hpp"
 #include "lion.hpp"
 #include "calib.hpp"
+#include "host.hpp"
 #include "muon_elem.hpp"
 #include "ns_gemm.hpp"
 
 using namespace ma;
 
-namespace {
+// what host.hpp declares
+namespace ma {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -45,40 +47,53 @@ int hip_fail(hipError_t e, const char* what) {
 // ----------------------------------------------------------------------------
 // kernel timing (ma_profile_*)
 // ----------------------------------------------------------------------------
-struct Profiler {
+static struct Profiler {
   bool active = false;
   int used = 0;
   std::vector<hipEvent_t> ev;   // 2 per launch
   std::vector<int> kind;        // per launch
 } g_prof;
 
-struct ProfScope {
-  int slot = -1;
-  hipStream_t s;
-  ProfScope(int k, hipStream_t st) : s(st) {
-    if (g_prof.active && g_prof.used < (int)g_prof.kind.size()) {
-      slot = g_prof.used++;
-      g_prof.kind[slot] = k;
-      (void)hipEventRecord(g_prof.ev[2 * slot], s);
-    }
+ProfScope::ProfScope(int k, hipStream_t st) : s(st) {
+  if (g_prof.active && g_prof.used < (int)g_prof.kind.size()) {
+    slot = g_prof.used++;
+    g_prof.kind[slot] = k;
+    (void)hipEventRecord(g_prof.ev[2 * slot], s);
   }
-  ~ProfScope() {
-    if (slot >= 0) (void)hipEventRecord(g_prof.ev[2 * slot + 1], s);
-  }
-};
+}
+
+ProfScope::~ProfScope() {
+  if (slot >= 0) (void)hipEventRecord(g_prof.ev[2 * slot + 1], s);
+}
+
+EntryMark::EntryMark(const char* what) { roctxRangePushA(what); }
+EntryMark::~EntryMark() { roctxRangePop(); }
+
+// The library's own per-device objects (the scratch array, the fork and join
+// events) are the current device's, and a launch goes to the current device:
+// a stream of another device must not be given either.
+int check_stream_device(void* stream, const char* what) {
+  int cur = 0;
+  hipError_t err = hipGetDevice(&cur);
+  if (err != hipSuccess) return hip_fail(err, "hipGetDevice");
+  if (!stream) return MA_OK;
+  hipDevice_t sd = 0;
+  err = hipStreamGetDevice(reinterpret_cast<hipStream_t>(stream), &sd);
+  if (err != hipSuccess) return hip_fail(err, "hipStreamGetDevice");
+  if ((int)sd != cur)
+    return fail(MA_ERR_INVALID_ARG, "%s belongs to device %d while device %d is current", what, (int)sd, cur);
+  return MA_OK;
+}
+
+}  // namespace ma
+
+namespace {
 
 // ----------------------------------------------------------------------------
 // roctx ranges on the calling thread (rocprofv3 --marker-trace): every entry
-// point that enqueues work is one range, and the Muon step's phases nest in
-// it. They span the host's enqueueing, not the GPU's execution.
+// point that enqueues work is one range (EntryMark), and the Muon step's
+// phases nest in it. They span the host's enqueueing, not the GPU's execution.
 // ----------------------------------------------------------------------------
-struct EntryMark {
-  explicit EntryMark(const char* what) { roctxRangePushA(what); }
-  ~EntryMark() { roctxRangePop(); }
-  EntryMark(const EntryMark&) = delete;
-  EntryMark& operator=(const EntryMark&) = delete;
-};
-
 struct PhaseMark {
   bool open = false;
   void enter(const char* what) {
@@ -955,22 +970,6 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
 void* g_scratch_ptr[kMaxDevices] = {};
-
-// The library's own per-device objects (the scratch array, the fork and join
-// events) are the current device's: a stream of another device must not be
-// given them.
-int check_stream_device(void* stream, const char* what) {
-  int cur = 0;
-  hipError_t err = hipGetDevice(&cur);
-  if (err != hipSuccess) return hip_fail(err, "hipGetDevice");
-  if (!stream) return MA_OK;
-  hipDevice_t sd = 0;
-  err = hipStreamGetDevice(reinterpret_cast<hipStream_t>(stream), &sd);
-  if (err != hipSuccess) return hip_fail(err, "hipStreamGetDevice");
-  if ((int)sd != cur)
-    return fail(MA_ERR_INVALID_ARG, "%s belongs to device %d while device %d is current", what, (int)sd, cur);
-  return MA_OK;
-}
 
 // The current device's address of `scratch` (looked up on the device's first
 // call, with that device current).

@@ -1,0 +1,93 @@
+// Launch descriptors of the operators around the optimizer step: embedding,
+// layer norm, 8-bit activation checkpoints and the weight gradient.
+#pragma once
+#include "common.hpp"
+
+namespace ma {
+
+// storage code of an operand held as an 8-bit checkpoint (kernel templates only)
+constexpr int DT_ACT8 = 2;
+
+// ---- embedding ----
+struct EmbedFwdArgs {
+  const void* table;
+  const void* tokens;
+  void* out;
+  int64_t rows, n_tokens;
+  int32_t cols, wide;   // wide: 8-byte tokens
+  float scale;
+};
+hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hipStream_t s);
+
+// Runs of the sorted tokens longer than this are summed in pieces of as many
+// sorted positions, one wave each, and joined in order.
+constexpr int kEmbedPiece = 64;
+struct EmbedBwdArgs {
+  const void* dout;
+  const void* tokens;
+  float* grad;
+  int64_t rows, n_tokens;
+  int32_t cols, wide, accumulate;
+  float scale;
+  // workspace: start / count of every row's run in the sorted order, the
+  // positions and rows in that order, the number of valid tokens, and two
+  // partial rows for each piece
+  int32_t *n_valid, *start, *count, *order, *keys;
+  float* partial;
+};
+size_t embed_bwd_workspace(int64_t rows, int64_t cols, int64_t n_tokens);
+void embed_bwd_carve(EmbedBwdArgs& a, unsigned char* ws);
+hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dout_dt, hipStream_t s);
+
+// ---- layer norm ----
+constexpr int64_t kMaxNormCols = 16384;   // what 1024 lanes hold in registers
+struct NormFwdArgs {
+  const void* x;
+  const float *gain, *bias;   // either may be null
+  void* y;
+  float* stats;               // 2 per row: mean, 1 / sqrt(var + eps)
+  uint8_t *q, *qscale;        // checkpoint of x, or null
+  int64_t rows;
+  int32_t cols;
+  float eps;
+};
+hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dt, int y_dt, hipStream_t s);
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* x;              // or q / qscale
+  const uint8_t *q, *qscale;
+  const float *stats, *gain;
+  void* dx;
+  float *dgain, *dbias;       // either may be null
+  float* partial;             // [blocks][2][cols]
+  int64_t rows;
+  int32_t cols, accumulate, blocks;
+};
+int norm_bwd_blocks(int64_t rows, int64_t cols);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dt, int dy_dt, int dx_dt, hipStream_t s);
+
+// ---- 8-bit activation checkpoints ----
+struct ActArgs {
+  const void* x;
+  void* out;
+  uint8_t *q, *qscale;
+  int64_t rows;
+  int32_t cols;
+};
+hipError_t launch_act_pack(const ActArgs& a, int x_dt, hipStream_t s);
+hipError_t launch_act_unpack(const ActArgs& a, int out_dt, hipStream_t s);
+
+// ---- weight gradient out of a checkpoint ----
+struct WgradArgs {
+  const void* dy;             // tokens x outs
+  const uint8_t *q, *qscale;  // tokens x ins
+  void* grad;                 // outs x ins
+  float* partial;             // [splits][outs][ins], splits > 1
+  int64_t tokens;
+  int32_t outs, ins, accumulate, splits;
+};
+int wgrad_splits(int64_t tokens, int64_t outs, int64_t ins, int dy_dt);
+hipError_t launch_wgrad(const WgradArgs& a, int dy_dt, int grad_dt, hipStream_t s);
+
+}  // namespace ma

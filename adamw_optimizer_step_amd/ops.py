@@ -1,0 +1,346 @@
+"""Python binding of the operators around the optimizer step: embedding, layer
+norm, 8-bit activation checkpoints and the weight gradient that reads one.
+
+They fill the gradient buffers that ``adamw_step``, ``lion_step`` and
+``muon_step`` read. As in ``api``, this is argument marshalling only: every
+computation runs in the HIP kernels of ``libmuon_adamw.so``, on the current
+stream of the tensors' device or on ``stream``. Tensors are contiguous; results
+that are not passed in are allocated for that stream. Names follow the C ABI
+(include/muon_adamw.h), which states each operator's rounding and limits.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+from typing import Optional, Tuple, Union
+
+import torch
+
+from . import _lib as L
+from .api import _DT, _dt
+
+_TOKENS = {torch.int32: 4, torch.int64: 8}
+_HERE = contextlib.nullcontext()
+
+
+def _check(what: str, t: torch.Tensor, dtypes, shape=None) -> torch.Tensor:
+    """`t` is a dense, contiguous tensor of one of `dtypes` and of `shape`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: unsupported dtype {t.dtype} ({', '.join(str(d) for d in dtypes)})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.layout != torch.strided or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t
+
+
+def _rows(what: str, t: torch.Tensor) -> Tuple[int, int]:
+    """(rows, cols) of a tensor normalised over its last dimension."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{what}: expected at least one column, got {tuple(t.shape)}")
+    cols = t.shape[-1]
+    return t.numel() // cols, cols
+
+
+def _device(*tensors: Optional[torch.Tensor]) -> torch.device:
+    """The one GPU that all tensors are on: the library takes raw device pointers."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got a tensor on {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"every tensor must be on {dev}, got one on {t.device}")
+    return dev
+
+
+class _Launch:
+    """The device and stream of a call: makes the tensors' device current, and
+    the call's stream too where one is given, so that what is allocated inside
+    belongs to it."""
+
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, dev: torch.device, stream):
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.dev, self.stream = dev, stream
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)   # makes its device current too
+        else:
+            self.ctx = _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)).cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, dev: torch.device) -> torch.Tensor:
+    """The caller's workspace, or one allocated for this call."""
+    return torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if given is None else given
+
+
+def _check_workspace(given: Optional[torch.Tensor]) -> None:
+    if given is not None:
+        _check("workspace", given, (torch.uint8,))
+
+
+# ---------------------------------------------------------------------------
+# embedding
+# ---------------------------------------------------------------------------
+def embedding_forward(table: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0, dtype: Optional[torch.dtype] = None,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``scale * table[tokens]`` as ``[*tokens.shape, cols]`` in ``dtype`` (the
+    table's by default). A token outside the table is ignored: zeros
+    (``ma_embedding_forward``)."""
+    _check("table", table, _DT)
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [rows, cols], got {tuple(table.shape)}")
+    _check("tokens", tokens, _TOKENS)
+    rows, cols = table.shape
+    shape = (*tokens.shape, cols)
+    if out is not None:
+        _check("out", out, (dtype,) if dtype is not None else _DT, shape)
+    elif dtype is not None and dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    dev = _device(table, tokens, out)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype or table.dtype, device=dev)
+        L.check(L.lib().ma_embedding_forward(table.data_ptr(), _dt(table), rows, cols, tokens.data_ptr(), _TOKENS[tokens.dtype],
+                                             tokens.numel(), scale, out.data_ptr(), _dt(out), s))
+    return out
+
+
+def embedding_workspace_size(rows: int, cols: int, n_tokens: int) -> int:
+    n = L.lib().ma_embedding_workspace_size(rows, cols, n_tokens)
+    if n == 0:
+        L.check(L.MA_ERR_INVALID_ARG)
+    return int(n)
+
+
+def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, scale: float = 1.0,
+                       accumulate: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The table's gradient in ``grad`` (fp32 ``[rows, cols]``, what an AdamW
+    segment reads), summed over equal tokens in a fixed order: written whole,
+    or with ``accumulate`` added to the rows that occur
+    (``ma_embedding_backward``). Returns ``grad``."""
+    _check("dout", dout, _DT)
+    _check("tokens", tokens, _TOKENS)
+    _check("grad", grad, (torch.float32,))
+    if grad.dim() != 2:
+        raise ValueError(f"grad: expected [rows, cols], got {tuple(grad.shape)}")
+    rows, cols = grad.shape
+    if tuple(dout.shape) != (*tokens.shape, cols):
+        raise ValueError(f"dout: expected shape {(*tokens.shape, cols)}, got {tuple(dout.shape)}")
+    _check_workspace(workspace)
+    n = tokens.numel()
+    dev = _device(dout, tokens, grad, workspace)
+    with _Launch(dev, stream) as s:
+        ws = _workspace(workspace, embedding_workspace_size(rows, cols, n), dev)
+        L.check(L.lib().ma_embedding_backward(dout.data_ptr(), _dt(dout), tokens.data_ptr(), _TOKENS[tokens.dtype], n, rows, cols,
+                                              scale, int(bool(accumulate)), grad.data_ptr(), ws.data_ptr(), ws.numel(), s))
+    return grad
+
+
+# ---------------------------------------------------------------------------
+# 8-bit activation checkpoints
+# ---------------------------------------------------------------------------
+class ActCheckpoint:
+    """An activation matrix ``[rows, cols]`` held in 8 bits: ``q`` (uint8
+    ``[rows, P]``, P = cols rounded up to a multiple of 128) and ``scale``
+    (uint8 ``[rows, P / 128]``), as ``act_pack`` writes them."""
+
+    __slots__ = ("q", "scale", "rows", "cols")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int):
+        blocks = -(-int(cols) // L.MA_ACT_BLOCK)
+        if cols < 1:
+            raise ValueError("a checkpoint has at least one column")
+        rows = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 2 else -1
+        self.q = _check("q", q, (torch.uint8,), (rows, blocks * L.MA_ACT_BLOCK))
+        self.scale = _check("scale", scale, (torch.uint8,), (rows, blocks))
+        self.rows, self.cols = rows, int(cols)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "ActCheckpoint":
+        """Room for the checkpoint of a ``[rows, cols]`` matrix."""
+        blocks = -(-cols // L.MA_ACT_BLOCK)
+        return cls(torch.empty((rows, blocks * L.MA_ACT_BLOCK), dtype=torch.uint8, device=device),
+                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols)
+
+    def nbytes(self) -> int:
+        return self.q.numel() + self.scale.numel()
+
+
+def _check_checkpoint(what: str, c: "ActCheckpoint", rows: int, cols: int) -> "ActCheckpoint":
+    if not isinstance(c, ActCheckpoint):
+        raise TypeError(f"{what}: expected an ActCheckpoint, got {type(c).__name__}")
+    if (c.rows, c.cols) != (rows, cols):
+        raise ValueError(f"{what}: a checkpoint of {(c.rows, c.cols)}, expected {(rows, cols)}")
+    return c
+
+
+def act_pack(x: torch.Tensor, out: Optional[ActCheckpoint] = None, stream=None) -> ActCheckpoint:
+    """The 8-bit checkpoint of ``x`` (its last dimension the columns, the
+    others flattened to rows; ``ma_act_pack``)."""
+    _check("x", x, _DT)
+    rows, cols = _rows("x", x)
+    if out is not None:
+        _check_checkpoint("out", out, rows, cols)
+    dev = _device(x, out.q, out.scale) if out is not None else _device(x)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = ActCheckpoint.empty(rows, cols, dev)
+        L.check(L.lib().ma_act_pack(x.data_ptr(), _dt(x), rows, cols, out.q.data_ptr(), out.scale.data_ptr(), s))
+    return out
+
+
+def act_unpack(checkpoint: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """The values a checkpoint holds as ``[rows, cols]`` in ``dtype`` (exact in
+    bf16 and fp32 alike; ``ma_act_unpack``)."""
+    if not isinstance(checkpoint, ActCheckpoint):
+        raise TypeError(f"expected an ActCheckpoint, got {type(checkpoint).__name__}")
+    rows, cols = checkpoint.rows, checkpoint.cols
+    if out is not None:
+        _check("out", out, _DT)
+        if out.dim() < 1 or out.shape[-1] != cols or out.numel() != rows * cols:
+            raise ValueError(f"out: expected {rows} rows of {cols} columns, got {tuple(out.shape)}")
+    elif dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    dev = _device(checkpoint.q, checkpoint.scale, out)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        L.check(L.lib().ma_act_unpack(checkpoint.q.data_ptr(), checkpoint.scale.data_ptr(), rows, cols, out.data_ptr(), _dt(out), s))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+def _param(what: str, t: Optional[torch.Tensor], cols: int) -> Optional[torch.Tensor]:
+    return None if t is None else _check(what, t, (torch.float32,), (cols,))
+
+
+def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                      dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                      stats: Optional[torch.Tensor] = None, checkpoint: Optional[ActCheckpoint] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Layer norm over the last dimension of ``x``; ``gain`` and ``bias`` are
+    fp32 ``[cols]``. Returns ``(y, stats)``: ``y`` in ``dtype`` (x's by default)
+    and fp32 ``[rows, 2]`` mean and reciprocal deviation, which the backward
+    pass reads. With ``checkpoint`` (``ActCheckpoint.empty(rows, cols, device)``)
+    the same pass also packs ``x`` into it (``ma_layernorm_forward``)."""
+    _check("x", x, _DT)
+    rows, cols = _rows("x", x)
+    _param("gain", gain, cols)
+    _param("bias", bias, cols)
+    if out is not None:
+        _check("out", out, (dtype,) if dtype is not None else _DT, x.shape)
+    elif dtype is not None and dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    if stats is not None:
+        _check("stats", stats, (torch.float32,), (rows, 2))
+    q = sc = None
+    if checkpoint is not None:
+        q, sc = _check_checkpoint("checkpoint", checkpoint, rows, cols).q, checkpoint.scale
+    dev = _device(x, gain, bias, out, stats, q, sc)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=dtype or x.dtype, device=dev)
+        if stats is None:
+            stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        L.check(L.lib().ma_layernorm_forward(x.data_ptr(), _dt(x), rows, cols, _ptr(gain), _ptr(bias), eps, out.data_ptr(), _dt(out),
+                                             stats.data_ptr(), _ptr(q), _ptr(sc), s))
+    return out, stats
+
+
+def layernorm_workspace_size(rows: int, cols: int) -> int:
+    n = L.lib().ma_layernorm_workspace_size(rows, cols)
+    if n == 0 and rows != 0:
+        L.check(L.MA_ERR_INVALID_ARG)
+    return int(n)
+
+
+def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], stats: torch.Tensor,
+                       gain: Optional[torch.Tensor] = None, dgain: Optional[torch.Tensor] = None,
+                       dbias: Optional[torch.Tensor] = None, accumulate: bool = False, dx: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The backward pass of ``layernorm_forward`` from ``dy``, ``stats`` and its
+    input ``x`` or that input's 8-bit checkpoint. Returns ``dx`` (x's type; dy's
+    for a checkpoint). The gradients of gain and bias go to the fp32 ``[cols]``
+    buffers ``dgain`` and ``dbias`` where given, written or, with
+    ``accumulate``, added to (``ma_layernorm_backward``)."""
+    _check("dy", dy, _DT)
+    rows, cols = _rows("dy", dy)
+    if isinstance(x, ActCheckpoint):
+        _check_checkpoint("x", x, rows, cols)
+        xt, q, sc, dx_dtype, xd = None, x.q, x.scale, dy.dtype, 0
+    else:
+        _check("x", x, _DT, dy.shape)
+        xt, q, sc, dx_dtype, xd = x, None, None, x.dtype, _dt(x)
+    _check("stats", stats, (torch.float32,), (rows, 2))
+    _param("gain", gain, cols)
+    _param("dgain", dgain, cols)
+    _param("dbias", dbias, cols)
+    if dx is not None:
+        _check("dx", dx, (dx_dtype,), dy.shape)
+    _check_workspace(workspace)
+    dev = _device(dy, xt, q, sc, stats, gain, dgain, dbias, dx, workspace)
+    sums = dgain is not None or dbias is not None
+    with _Launch(dev, stream) as s:
+        if dx is None:
+            dx = torch.empty(dy.shape, dtype=dx_dtype, device=dev)
+        ws = _workspace(workspace, layernorm_workspace_size(rows, cols), dev) if sums else None
+        L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, _ptr(q), _ptr(sc), rows, cols, stats.data_ptr(),
+                                              _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
+                                              _ptr(ws), ws.numel() if sums else 0, s))
+    return dx
+
+
+# ---------------------------------------------------------------------------
+# weight gradient
+# ---------------------------------------------------------------------------
+def act_weight_grad_workspace_size(tokens: int, outs: int, ins: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace (0: none needed) for dy of ``dtype``."""
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    n = L.lib().ma_act_weight_grad_workspace_size(tokens, outs, ins, _DT[dtype])
+    if n == 0 and (min(outs, ins) < 1 or tokens < 0):
+        L.check(L.MA_ERR_INVALID_ARG)
+    return int(n)
+
+
+def act_weight_grad(dy: torch.Tensor, x: ActCheckpoint, grad: torch.Tensor, accumulate: bool = False,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The weight gradient of ``y = x W^T`` in ``grad`` (``[outs, ins]``, bf16
+    or fp32: a matrix of a ``MuonGroup``'s gradients), out of the 8-bit
+    checkpoint of ``x``: ``grad (+)= dy^T x`` (``ma_act_weight_grad``). ``dy``:
+    ``[..., outs]`` with as many rows as the checkpoint. Returns ``grad``."""
+    _check("dy", dy, _DT)
+    tokens, outs = _rows("dy", dy)
+    if not isinstance(x, ActCheckpoint):
+        raise TypeError(f"x: expected an ActCheckpoint, got {type(x).__name__}")
+    if x.rows != tokens:
+        raise ValueError(f"dy has {tokens} rows, the checkpoint {x.rows}")
+    _check("grad", grad, _DT, (outs, x.cols))
+    _check_workspace(workspace)
+    dev = _device(dy, x.q, x.scale, grad, workspace)
+    with _Launch(dev, stream) as s:
+        need = act_weight_grad_workspace_size(tokens, outs, x.cols, dy.dtype)
+        ws = _workspace(workspace, need, dev) if need or workspace is not None else None
+        L.check(L.lib().ma_act_weight_grad(dy.data_ptr(), _dt(dy), x.q.data_ptr(), x.scale.data_ptr(), tokens, outs, x.cols,
+                                           grad.data_ptr(), _dt(grad), int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0, s))
+    return grad

@@ -330,6 +330,94 @@ typedef struct {
  * segment. */
 int ma_lion_step(const ma_lion_segment* segments, int32_t n_segments, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the step: what fills the gradient buffers that the
+ * steps above read. The embedding's and the norms' gradients are flat fp32
+ * buffers (AdamW and Lion segments), the weight gradient is a row-major
+ * outs x ins matrix of either storage type (a Muon group's grads[i]). All
+ * tensors are dense and row-major and start at any multiple of their element
+ * size; outputs may not overlap any other buffer of the call
+ * (MA_ERR_INVALID_ARG). Sums are fp32, in an order that depends on the sizes
+ * alone, and each output is rounded once to its type: a call repeated on the
+ * same inputs gives the same bits. accumulate = 1 adds to the gradient that is
+ * already there (in fp32, before the one rounding); 0 writes it whole. `stream`
+ * must belong to the current device (MA_ERR_INVALID_ARG). Every call may be
+ * captured in a HIP graph; a graph keeps the workspace it was captured with,
+ * and graphs or calls that may overlap need one each.
+ * ------------------------------------------------------------------------- */
+
+/* out[i,:] = scale * table[tokens[i],:] for i < n_tokens. table: rows x cols;
+ * tokens: n_tokens integers of token_bytes (4 or 8, signed); out: n_tokens x
+ * cols. A token outside 0..rows-1 is ignored: its output row is zero, and it
+ * takes no part in the gradient (a row of another rank's shard, a masked
+ * position). Limits: rows, cols <= 2^24, n_tokens <= 2^25, rows * cols and
+ * n_tokens * cols <= 2^38; scale finite. */
+int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, int64_t cols, const void* tokens,
+                         int32_t token_bytes, int64_t n_tokens, float scale, void* out, int32_t out_dtype, void* stream);
+
+/* grad[v,:] = scale * sum of dout[i,:] over the i with tokens[i] == v, for
+ * every row v < rows (zero where there is none). With accumulate the rows that
+ * occur are added to and no other row is touched. dout: n_tokens x cols; grad:
+ * rows x cols, fp32. The tokens are sorted first (stable, by kernels of this
+ * call): runs of up to 64 are summed in ascending i, longer ones in pieces that
+ * are joined in order. workspace: at least ma_embedding_workspace_size bytes
+ * (0 from that function: invalid sizes), MA_WORKSPACE_ALIGN aligned. */
+size_t ma_embedding_workspace_size(int64_t rows, int64_t cols, int64_t n_tokens);
+int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* tokens, int32_t token_bytes, int64_t n_tokens,
+                          int64_t rows, int64_t cols, float scale, int32_t accumulate, float* grad, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Layer norm over the last dimension, per row of x (rows x cols, cols <= 16384):
+ *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   y = (x - mean) * rstd * gain + bias        gain, bias: cols fp32 values, either may be null
+ * stats (rows x 2 fp32, 8-byte aligned) receives mean and rstd for the backward
+ * pass. With ckpt_q and ckpt_scale (both or neither) the same pass also writes
+ * the 8-bit checkpoint of x, as ma_act_pack would. */
+int ma_layernorm_forward(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, const float* gain, const float* bias,
+                         float eps, void* y, int32_t y_dtype, float* stats, uint8_t* ckpt_q, uint8_t* ckpt_scale,
+                         void* stream);
+
+/* Its backward pass from dy, stats and either x or x's checkpoint (the other
+ * null): with xh = (x - mean) * rstd and g = dy * gain (gain may be null),
+ *   dx = rstd * (g - mean(g) - xh * mean(g * xh))
+ *   dgain (+)= sum over rows of dy * xh;  dbias (+)= sum over rows of dy
+ * dx has x's type, or dy's where x is a checkpoint. dgain and dbias (cols fp32
+ * values) may each be null; with both null no workspace is needed, else at
+ * least ma_layernorm_workspace_size bytes (0 also for rows = 0). accumulate
+ * applies to dgain and dbias. */
+size_t ma_layernorm_workspace_size(int64_t rows, int64_t cols);
+int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const uint8_t* ckpt_q,
+                          const uint8_t* ckpt_scale, int64_t rows, int64_t cols, const float* stats, const float* gain,
+                          void* dx, int32_t dx_dtype, float* dgain, float* dbias, int32_t accumulate, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* 8-bit activation checkpoints. q (rows x P bytes, P = cols rounded up to a
+ * multiple of MA_ACT_BLOCK, 16-byte aligned, zero beyond cols) holds e4m3 (OCP)
+ * values, scale (rows x P / MA_ACT_BLOCK bytes) a power of two for each block of
+ * MA_ACT_BLOCK columns: the byte s stands for 2^(s - 127). Packing takes the
+ * least exponent in -117..120 with amax <= 448 * 2^e over the block's finite
+ * values and rounds x / 2^e to nearest even, within 448 (240 at e = 120, so that
+ * every value held is finite in bf16 and fp32). NaN and infinities are held as
+ * NaN. Every held value is exact in bf16: unpacking rounds nothing, and the
+ * error against x is at most 2^-4 |x|, or 2^-10 * 2^e for values below the
+ * block's e4m3 normal range (2^-6 * 2^e). */
+#define MA_ACT_BLOCK 128
+int ma_act_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, uint8_t* q, uint8_t* scale, void* stream);
+int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, void* out, int32_t out_dtype,
+                  void* stream);
+
+/* The weight gradient of a linear layer y = x W^T out of x's checkpoint:
+ *   grad[n,k] (+)= sum over tokens t of dy[t,n] * x[t,k]
+ * dy: tokens x outs; q, scale: the checkpoint of x (tokens x ins) as written by
+ * ma_act_pack; grad: outs x ins. The held values are used as they are (no
+ * second rounding) and dy at its full precision; products are summed in fp32.
+ * Limits: tokens <= 2^25, outs, ins <= 2^24, outs * ins <= 2^31. workspace: at
+ * least ma_act_weight_grad_workspace_size bytes, which may be 0. */
+size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype);
+int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const uint8_t* scale, int64_t tokens,
+                       int64_t outs, int64_t ins, void* grad, int32_t grad_dtype, int32_t accumulate, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Status text for a code, and the calling thread's last error message. */
 const char* ma_status_string(int status);
 const char* ma_last_error(void);
@@ -357,7 +445,11 @@ typedef enum {
   MA_K_ADAMW = 7,
   MA_K_LION = 8,
   MA_K_AXPY_UPDATE = 9, /* the last AXPY of a step with the update fused into it */
-  MA_K_COUNT = 10
+  MA_K_EMBEDDING = 10,  /* one ma_embedding_* call, all its launches */
+  MA_K_LAYERNORM = 11,  /* one ma_layernorm_* call */
+  MA_K_ACT = 12,        /* ma_act_pack, ma_act_unpack */
+  MA_K_WEIGHT_GRAD = 13, /* one ma_act_weight_grad call */
+  MA_K_COUNT = 14
 } ma_kernel_kind;
 
 int ma_profile_begin(int32_t max_launches);
