@@ -175,7 +175,7 @@ int ma_layernorm_forward(const void* x, int32_t x_dtype, int64_t rows, int64_t c
 
 size_t ma_layernorm_workspace_size(int64_t rows, int64_t cols) {
   if (check_matrix("ma_layernorm_workspace_size", rows, 0, kMaxRows, cols, kMaxNormCols)) return 0;
-  return (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * cols * 4, MA_WORKSPACE_ALIGN);
+  return (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * round_up(cols, 32) * 4, MA_WORKSPACE_ALIGN);
 }
 
 int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const uint8_t* ckpt_q, const uint8_t* ckpt_scale,
@@ -195,7 +195,7 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
     return fail(MA_ERR_UNSUPPORTED, "%s: dx has the type of x, or of dy where x is a checkpoint", fn);
   const int64_t pitch = act_pitch(cols);
   const bool sums = dgain || dbias;
-  const size_t need = sums ? (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * cols * 4, MA_WORKSPACE_ALIGN) : 0;
+  const size_t need = sums ? (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * round_up(cols, 32) * 4, MA_WORKSPACE_ALIGN) : 0;
   const Buf bufs[] = {{dy, rows * cols * dt_size(dy_dtype), (int)dt_size(dy_dtype), false, false, "dy"},
                       {x, held ? 0 : rows * cols * dt_size(x_dtype), held ? 1 : (int)dt_size(x_dtype), false, false, "x"},
                       {ckpt_q, rows * pitch, 16, false, !held, "x and the checkpoint's q"},

@@ -18,7 +18,7 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int wide, int64_
 // forward: LPR lanes per output row, R rows per lane group at a time, so that
 // R independent row reads are in flight behind their R token reads.
 // ---------------------------------------------------------------------------
-template <int TD, int OD, int LPR>
+template <int TD, int OD, int LPR, bool NT>
 __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwdArgs a) {
   constexpr int R = 4, GROUPS = 256 / LPR;
   const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
@@ -41,22 +41,27 @@ __global__ void __launch_bounds__(256) k_embed_fwd(const EmbedFwdArgs a) {
     for (int r = 0; r < R; ++r) {
       if (r0 + r >= a.n_tokens) break;
       float v[8];
-      raw_f32<TD>(x[r], v);
+      raw_f32_row<TD>(x[r], col, a.cols, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = in[r] ? v[e] * a.scale : 0.0f;
-      store_row<OD>(elem_ptr<OD>(a.out, (r0 + r) * a.cols), col, a.cols, v);
+      store_row<OD, NT>(elem_ptr<OD>(a.out, (r0 + r) * a.cols), col, a.cols, v);
     }
   }
 }
 
-template <int TD, int OD>
+template <int TD, int OD, bool NT>
 static hipError_t embed_fwd(const EmbedFwdArgs& a, hipStream_t s) {
   const int chunks = (a.cols + 7) / 8;
   auto grid = [&](int lpr) { const int64_t per = 256 / lpr * 4; return dim3((unsigned)((a.n_tokens + per - 1) / per)); };
-  if (chunks <= 16) hipLaunchKernelGGL((k_embed_fwd<TD, OD, 16>), grid(16), dim3(256), 0, s, a);
-  else if (chunks <= 32) hipLaunchKernelGGL((k_embed_fwd<TD, OD, 32>), grid(32), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_embed_fwd<TD, OD, 64>), grid(64), dim3(256), 0, s, a);
+  if (chunks <= 16) hipLaunchKernelGGL((k_embed_fwd<TD, OD, 16, NT>), grid(16), dim3(256), 0, s, a);
+  else if (chunks <= 32) hipLaunchKernelGGL((k_embed_fwd<TD, OD, 32, NT>), grid(32), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_embed_fwd<TD, OD, 64, NT>), grid(64), dim3(256), 0, s, a);
   return hipGetLastError();
+}
+template <int TD, int OD>
+static hipError_t embed_fwd(const EmbedFwdArgs& a, hipStream_t s) {
+  const bool stream = a.n_tokens * a.cols * (elem_bytes<TD>() + elem_bytes<OD>()) > kStreamBytes;
+  return stream ? embed_fwd<TD, OD, true>(a, s) : embed_fwd<TD, OD, false>(a, s);
 }
 
 hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hipStream_t s) {
@@ -66,51 +71,124 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hip
 }
 
 // ---------------------------------------------------------------------------
-// backward, 1: the tokens' positions sorted by (row mod NB, row / NB), stable,
-// in one launch. Block b of NB (a power of two) owns the rows v = b mod NB
-// (interleaved: frequent rows with neighbouring ids go to different blocks).
-// It reads all tokens twice. First pass: how many valid tokens belong to
-// earlier blocks (where its own part of the sorted order begins), and how
-// often each of its rows occurs in each wave's sixteenth of the tokens.
-// Second pass: every wave writes its tokens' positions behind those of the
-// waves before it. No global atomics, and the order is ascending position.
+// backward, 1: the tokens' positions sorted by slot, stable, in one launch. Row
+// v has slot (v mod NB) * M + v / NB with M = ceil(rows / NB): block b of NB (a
+// power of two) owns the M slots b M .., the rows b mod NB (interleaved, so that
+// frequent rows with neighbouring ids go to different blocks). It reads all
+// tokens, each of its 16 waves a contiguous sixteenth: it counts how many valid
+// tokens belong to earlier blocks (where its own part of the sorted order
+// begins) and keeps its own tokens in LDS, a list per wave. Each wave numbers its
+// list's tokens within their rows, 64 at a time; the rows' counts are added up
+// over the waves, and every token's position goes to its place. A wave whose
+// list overflows (a few rows have most of the tokens) reads its share again.
+// No global atomics, and the order is ascending position.
 // ---------------------------------------------------------------------------
-constexpr int kBinThreads = 1024, kBinWaves = kBinThreads / 64, kBinRows = 512;
+constexpr int kBinThreads = 1024, kBinWaves = kBinThreads / 64, kBinRows = 512, kBinBits = 9, kBinList = 1024;
 
-__global__ void __launch_bounds__(kBinThreads) k_embed_bin(const EmbedBwdArgs a, int log2nb) {
-  __shared__ uint32_t hist[kBinWaves][kBinRows];
-  __shared__ uint32_t scan[kBinRows];
-  __shared__ uint32_t wsum[kBinWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t nb = (int64_t)1 << log2nb, me = blockIdx.x;
-  const int mine = (int)((a.rows - me + nb - 1) >> log2nb);   // rows owned, <= kBinRows; 0 if me >= rows
-  for (int i = tid; i < kBinWaves * kBinRows; i += kBinThreads) (&hist[0][0])[i] = 0;
-  __syncthreads();
-  const int64_t seg = round_up((a.n_tokens + kBinWaves - 1) / kBinWaves, 64);
-  const int64_t i0 = wave * seg, i1 = i0 + seg < a.n_tokens ? i0 + seg : a.n_tokens;
-  uint32_t less = 0;
-  constexpr int U = 8;
-  for (int64_t i = i0; i < i1; i += 64 * U) {
-    int64_t v[U];
+// The next numbers of the lanes' rows: a lane with own = true gets next[bin] plus
+// the number of lower lanes with the same row, and next[bin] moves on by all of them.
+__device__ __forceinline__ uint32_t embed_next(volatile uint32_t* next, bool own, int bin) {
+  // the lanes with the same row as this one, by the bits of its index
+  uint64_t same = __ballot(own);
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = i + u * 64 + lane < i1 ? token_at(a.tokens, a.wide, i + u * 64 + lane) : -1;
+  for (int i = 0; i < kBinBits; ++i) {
+    const uint64_t m = __ballot(bin >> i & 1);
+    same &= bin >> i & 1 ? m : ~m;
+  }
+  const int rank = __builtin_popcountll(same & (((uint64_t)1 << (threadIdx.x & 63)) - 1));
+  const uint32_t at = next[bin];
+  if (own && rank == 0) next[bin] = at + (uint32_t)__builtin_popcountll(same);
+  return at + rank;
+}
+
+// The 64 * U tokens from `first` of a share that ends at n, token u * 64 + lane in v[u], as
+// 32 bits: 0xFFFFFFFF (no row) for one outside them or past the end.
+template <bool WIDE, int U>
+__device__ __forceinline__ void tokens32(const void* share, int first, int n, int lane, uint32_t (&v)[U]) {
+  if (first + 64 * U <= n) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = v[u] >= 0 && v[u] < a.rows;
-      const int64_t b = v[u] & (nb - 1);
-      less += in && b < me;
-      if (in && b == me) atomicAdd(&hist[wave][v[u] >> log2nb], 1u);
+      if constexpr (WIDE) {
+        const uint2 t = reinterpret_cast<const uint2*>(share)[first + u * 64 + lane];
+        v[u] = t.y ? 0xFFFFFFFFu : t.x;
+      } else {
+        v[u] = reinterpret_cast<const uint32_t*>(share)[first + u * 64 + lane];
+      }
     }
+    return;
   }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) less += __shfl_xor(less, o, 64);
+  for (int u = 0; u < U; ++u) {
+    const int i = first + u * 64 + lane;
+    v[u] = 0xFFFFFFFFu;
+    if (i < n) {
+      if constexpr (WIDE) {
+        const uint2 t = reinterpret_cast<const uint2*>(share)[i];
+        v[u] = t.y ? 0xFFFFFFFFu : t.x;
+      } else {
+        v[u] = reinterpret_cast<const uint32_t*>(share)[i];
+      }
+    }
+  }
+}
+
+template <bool WIDE>
+__global__ void __launch_bounds__(kBinThreads) k_embed_bin(const EmbedBwdArgs a) {
+  __shared__ uint32_t hist[kBinWaves][kBinRows];
+  __shared__ uint32_t list[kBinWaves][kBinList];   // (offset in the wave's share) * kBinRows + owned row
+  __shared__ uint16_t nth[kBinWaves][kBinList];    // which of its row's tokens in the share it is
+  __shared__ uint32_t wsum[kBinWaves], scan[kBinWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t mask = ((uint32_t)1 << a.log2nb) - 1, me = blockIdx.x, rows = (uint32_t)a.rows;
+  for (int i = lane; i < kBinRows; i += 64) hist[wave][i] = 0;
+  const int seg = (int)round_up((a.n_tokens + kBinWaves - 1) / kBinWaves, 64);   // <= 2^21: an offset and a row fit 32 bits
+  const int64_t i0 = (int64_t)wave * seg;
+  const int n = (int)(i0 + seg < a.n_tokens ? seg : (i0 < a.n_tokens ? a.n_tokens - i0 : 0));
+  const void* share = reinterpret_cast<const unsigned char*>(a.tokens) + i0 * (WIDE ? 8 : 4);
+  uint32_t less = 0;
+  int kept = 0;
+  constexpr int U = 8;
+  for (int i = 0; i < n; i += 64 * U) {
+    uint32_t v[U];
+    tokens32<WIDE, U>(share, i, n, lane, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t b = v[u] < rows ? v[u] & mask : 0xFFFFFFFFu;
+      less += (uint32_t)__builtin_popcountll(__ballot(b < me));
+      const uint64_t owns = __ballot(b == me);
+      if (!owns) continue;
+      const int k = kept + __builtin_popcountll(owns & (((uint64_t)1 << lane) - 1));
+      if (b == me && k < kBinList) list[wave][k] = (uint32_t)(i + u * 64 + lane) * kBinRows + (v[u] >> a.log2nb);
+      kept += __builtin_popcountll(owns);
+    }
+  }
+  // each of them counted at its row: f(lane's token is one, its row, its place in the list or its offset)
+  const bool listed = kept <= kBinList;
+  auto own_tokens = [&](auto&& f) __attribute__((always_inline)) {
+    if (listed) {
+      for (int k = 0; k < kept; k += 64) {
+        const uint32_t x = k + lane < kept ? list[wave][k + lane] : 0u;
+        f(k + lane < kept, (int)(x % kBinRows), (int)(x / kBinRows), k + lane);
+      }
+    } else {
+      for (int i = 0; i < n; i += 64) {
+        uint32_t v[1];
+        tokens32<WIDE, 1>(share, i, n, lane, v);
+        f(v[0] < rows && (v[0] & mask) == me, (int)(v[0] >> a.log2nb) & (kBinRows - 1), i + lane, 0);
+      }
+    }
+  };
+  own_tokens([&](bool own, int bin, int, int k) {
+    const uint32_t at = embed_next(hist[wave], own, bin);
+    if (own && listed) nth[wave][k] = (uint16_t)at;
+  });
   if (lane == 0) wsum[wave] = less;
   __syncthreads();
   uint32_t base = 0;
 #pragma unroll
   for (int w = 0; w < kBinWaves; ++w) base += wsum[w];
-  // per row: exclusive counts over the waves, and the row's total
-  uint32_t total = 0;
+  // per row (thread): exclusive counts over the waves, the total, and the totals' scan over the owned rows
+  uint32_t total = 0, upto = 0;
   if (tid < kBinRows) {
 #pragma unroll
     for (int w = 0; w < kBinWaves; ++w) {
@@ -118,74 +196,60 @@ __global__ void __launch_bounds__(kBinThreads) k_embed_bin(const EmbedBwdArgs a,
       hist[w][tid] = total;
       total += h;
     }
-    scan[tid] = total;
   }
-  // inclusive scan of the totals over the owned rows
+  upto = total;
 #pragma unroll
-  for (int o = 1; o < kBinRows; o <<= 1) {
-    __syncthreads();
-    const uint32_t x = tid < kBinRows && tid >= o ? scan[tid - o] : 0u;
-    __syncthreads();
-    if (tid < kBinRows) scan[tid] += x;
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t x = __shfl_up(upto, o, 64);
+    upto += lane >= o ? x : 0u;
   }
+  if (lane == 63) scan[wave] = upto;
   __syncthreads();
-  if (tid < mine) {
-    const int64_t v = ((int64_t)tid << log2nb) + me;
-    a.start[v] = (int32_t)(base + scan[tid] - total);
-    a.count[v] = (int32_t)total;
+#pragma unroll
+  for (int w = 0; w < kBinRows / 64; ++w) upto += w < wave ? scan[w] : 0u;
+  const uint32_t at = base + upto - total;
+  const int32_t slot0 = (int32_t)me * a.per_block;
+  if (tid < a.per_block) {
+    a.start[slot0 + tid] = (int32_t)at;
+    a.count[slot0 + tid] = (int32_t)total;
   }
-  if (me == nb - 1 && tid == 0) *a.n_valid = (int32_t)(base + scan[kBinRows - 1]);
   if (tid < kBinRows) {
-    const uint32_t at = base + scan[tid] - total;
+    if (me == mask && tid == kBinRows - 1) *a.n_valid = (int32_t)(base + upto);
 #pragma unroll
     for (int w = 0; w < kBinWaves; ++w) hist[w][tid] += at;
   }
   __syncthreads();
-  for (int64_t i = i0; i < i1; i += 64 * U) {
-    int64_t v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = i + u * 64 + lane < i1 ? token_at(a.tokens, a.wide, i + u * 64 + lane) : -1;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool own = v[u] >= 0 && v[u] < a.rows && (v[u] & (nb - 1)) == me;
-      const int bin = (int)(v[u] >> log2nb);
-      uint64_t left = __ballot(own);
-      // one step per different row among the 64 tokens
-      while (left) {
-        const int first = __builtin_ctzll(left);
-        const int bin0 = __builtin_amdgcn_readlane(bin, first);
-        const uint64_t same = __ballot(own && bin == bin0);
-        volatile uint32_t& next = hist[wave][bin0];
-        const uint32_t at = next;
-        if (own && bin == bin0) {
-          const uint32_t k = at + __builtin_popcountll(same & (((uint64_t)1 << lane) - 1));
-          a.order[k] = (int32_t)(i + u * 64 + lane);
-          a.keys[k] = (int32_t)v[u];
-        }
-        if (lane == first) next = at + (uint32_t)__builtin_popcountll(same);
-        left &= ~same;
-      }
+  own_tokens([&](bool own, int bin, int offset, int k) {
+    uint32_t to;
+    if (listed) to = own ? hist[wave][bin] + nth[wave][k] : 0u;
+    else to = embed_next(hist[wave], own, bin);
+    if (own) {
+      a.order[to] = (int32_t)(i0 + offset);
+      a.keys[to] = slot0 + bin;
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
-// backward, 2: the sums. One wave per row of the table and slice of 512 * CH
-// columns sums the row's run (at most kEmbedPiece tokens) and writes it, zeros
-// for an empty one; when accumulating, one wave per sorted position, of which
-// those at the start of a run work. Longer runs are summed by the piece waves
-// (the launch's first blocks), one per kEmbedPiece sorted positions: the part
-// of a long run that its first position belongs to goes to partial row 2p, that
-// of another long run that its last position belongs to to 2p + 1 (no third
-// one fits), and k_embed_join adds a run's parts in order.
+// backward, 2: the sums, a slice of 512 * CH columns per wave. A wave takes
+// kEmbedGroup consecutive slots, whose positions are consecutive in the sorted
+// order: it loads their counts and positions at once, sums each row's run (at
+// most kEmbedPiece tokens) and writes it, zeros for an empty one, or adds it to
+// a row that occurs. Longer runs are summed by the piece waves (the launch's
+// first blocks), one per kEmbedPiece sorted positions: the part of a long run
+// that its first position belongs to goes to partial row 2p, that of another
+// long run that its last position belongs to to 2p + 1 (no third one fits), and
+// k_embed_join adds a run's parts in order.
 // ---------------------------------------------------------------------------
+constexpr int kEmbedGroup = 2;
+
 template <int DD, int CH>
 __device__ __forceinline__ void embed_sum(const EmbedBwdArgs& a, int32_t pos, int from, int to, int col, float (&acc)[CH][8]) {
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[c][e] = 0.0f;
-  constexpr int U = 4;
+  constexpr int U = (DD == DT_BF16 ? 16 : 8) / CH;   // 64 registers of rows in flight; each row is read once (non-temporal)
   for (int j = from; j < to; j += U) {
     Raw8<DD> x[U][CH];
 #pragma unroll
@@ -195,7 +259,7 @@ __device__ __forceinline__ void embed_sum(const EmbedBwdArgs& a, int32_t pos, in
         const unsigned char* row = elem_ptr<DD>(a.dout, p * a.cols);
 #pragma unroll
         for (int c = 0; c < CH; ++c)
-          x[u][c] = col + c * 512 < a.cols ? raw_load_row<DD>(row, col + c * 512, a.cols) : raw_zero<DD>();
+          x[u][c] = col + c * 512 < a.cols ? raw_load_row<DD, true>(row, col + c * 512, a.cols) : raw_zero<DD>();
       }
     }
 #pragma unroll
@@ -204,7 +268,7 @@ __device__ __forceinline__ void embed_sum(const EmbedBwdArgs& a, int32_t pos, in
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           float v[8];
-          raw_f32<DD>(x[u][c], v);
+          raw_f32_row<DD>(x[u][c], col + c * 512, a.cols, v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[c][e] += v[e];
         }
@@ -242,82 +306,117 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int pie
     }
     return;
   }
-  const int64_t item = (int64_t)(blockIdx.x - piece_blocks) * 4 + wave;
-  int64_t v = item;
-  if constexpr (ACC) {
-    if (item >= *a.n_valid) return;
-    v = a.keys[item];
-  } else {
-    if (item >= a.rows) return;
-  }
-  const int64_t s = a.start[v];
-  const int c = a.count[v];
-  if (c > kEmbedPiece || (ACC && s != item)) return;
-  const int32_t pos = lane < c ? a.order[s + lane] : 0;
-  embed_sum<DD, CH>(a, pos, 0, c, col, acc);
-  unsigned char* out = reinterpret_cast<unsigned char*>(a.grad + v * a.cols);
+  // the wave's slots: the owning block and the first of its rows; waves that run
+  // together write neighbouring rows
+  const int32_t item = (int32_t)(blockIdx.x - piece_blocks) * 4 + wave;
+  const int32_t owner = item & ((1 << a.log2nb) - 1), bin0 = (item >> a.log2nb) * kEmbedGroup;
+  const int have = a.per_block - bin0 < kEmbedGroup ? a.per_block - bin0 : kEmbedGroup;
+  const int32_t slot0 = owner * a.per_block + bin0;
+  const int32_t starts = lane < have ? a.start[slot0 + lane] : 0, counts = lane < have ? a.count[slot0 + lane] : 0;
+  for (int r = 0; r < have; ++r) {
+    const int64_t v = ((int64_t)(bin0 + r) << a.log2nb) + owner;
+    if (v >= a.rows) break;
+    const int c = __builtin_amdgcn_readlane(counts, r);
+    if (c > kEmbedPiece || (ACC && c == 0)) continue;
+    const int64_t s = __builtin_amdgcn_readlane(starts, r);
+    const int32_t pos = lane < c ? a.order[s + lane] : 0;
+    embed_sum<DD, CH>(a, pos, 0, c, col, acc);
+    unsigned char* out = reinterpret_cast<unsigned char*>(a.grad + v * a.cols);
 #pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int cc = col + k * 512;
-    if (cc >= a.cols) continue;
-    float old[8] = {};
-    if constexpr (ACC) raw_f32<DT_F32>(raw_load_row<DT_F32>(out, cc, a.cols), old);
+    for (int k = 0; k < CH; ++k) {
+      const int cc = col + k * 512;
+      if (cc >= a.cols) continue;
+      float old[8] = {};
+      if constexpr (ACC) raw_f32_row<DT_F32>(raw_load_row<DT_F32>(out, cc, a.cols), cc, a.cols, old);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[k][e] = ACC ? __fadd_rn(old[e], __fmul_rn(acc[k][e], a.scale)) : acc[k][e] * a.scale;
-    store_row<DT_F32, !ACC>(out, cc, a.cols, acc[k]);
+      for (int e = 0; e < 8; ++e) acc[k][e] = ACC ? __fadd_rn(old[e], __fmul_rn(acc[k][e], a.scale)) : acc[k][e] * a.scale;
+      store_row<DT_F32>(out, cc, a.cols, acc[k]);
+    }
   }
 }
 
-// The long run that starts in piece p, if one does: 16 waves sum its parts in
-// 16 contiguous shares, 256 columns each, and the shares are added in order.
-__global__ void __launch_bounds__(1024) k_embed_join(const EmbedBwdArgs a) {
-  __shared__ float part[16][256];
-  const int64_t p = blockIdx.x, first = p * kEmbedPiece;
-  const int64_t left = *a.n_valid - first;
-  if (left <= kEmbedPiece) return;   // no run of this piece goes on in another
-  const int32_t v = a.keys[first + kEmbedPiece - 1];
-  const int64_t s = a.start[v], c = a.count[v];
-  if (c <= kEmbedPiece || s < first) return;
-  const int64_t last = (s + c - 1) / kEmbedPiece;
+// The long runs that start in one of the block's kJoinPieces pieces (at most one
+// in each): the block's waves sum a run's parts in as many contiguous shares,
+// 256 columns per block, and the shares are added in order.
+constexpr int kJoinWaves = 8, kJoinPieces = 4;
+__global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdArgs a) {
+  __shared__ float4 part[kJoinWaves][64];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t n = last - p + 1, share = (n + 15) / 16;
-  const int64_t q0 = p + wave * share, q1 = q0 + share < last + 1 ? q0 + share : last + 1;
-  const int col = blockIdx.y * 256 + lane;
-  float acc[4] = {};
-#pragma unroll 4
-  for (int64_t q = q0; q < q1; ++q) {
-    const float* src = a.partial + (2 * q + (q == p && s > first)) * a.cols;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (col + 64 * k < a.cols) acc[k] += src[col + 64 * k];
+  const int64_t n_valid = *a.n_valid;
+  // lane i: does a long run start in piece i? (the last piece's last run goes on nowhere)
+  const int64_t mine = (int64_t)blockIdx.x * kJoinPieces + lane;
+  bool starts = false;
+  int32_t slot = 0, s = 0, c = 0;
+  if (lane < kJoinPieces && n_valid - mine * kEmbedPiece > kEmbedPiece) {
+    slot = a.keys[(mine + 1) * kEmbedPiece - 1];
+    s = a.start[slot];
+    c = a.count[slot];
+    starts = c > kEmbedPiece && s >= mine * kEmbedPiece;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) part[wave][lane + 64 * k] = acc[k];
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) t += part[w][threadIdx.x];
+  const int col = blockIdx.y * 256 + lane * 4;
+  const bool whole = col + 4 <= a.cols;
+  for (uint64_t todo = __ballot(starts); todo; todo &= todo - 1) {
+    const int i = __builtin_ctzll(todo);
+    const int64_t p = (int64_t)blockIdx.x * kJoinPieces + i;
+    const int64_t rs = __builtin_amdgcn_readlane(s, i), rc = __builtin_amdgcn_readlane(c, i);
+    const int64_t last = (rs + rc - 1) / kEmbedPiece;
+    const int64_t n = last - p + 1, share = (n + kJoinWaves - 1) / kJoinWaves;
+    const int64_t q0 = p + wave * share, q1 = q0 + share < last + 1 ? q0 + share : last + 1;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    typedef typename U16<DT_F32>::T V;
+    if (whole) {
+#pragma unroll 8
+      for (int64_t q = q0; q < q1; ++q) {
+        const u32x4_t u = *reinterpret_cast<const V*>(a.partial + (2 * q + (q == p && rs > p * kEmbedPiece)) * a.cols + col);
+        acc.x += __uint_as_float(u[0]); acc.y += __uint_as_float(u[1]); acc.z += __uint_as_float(u[2]); acc.w += __uint_as_float(u[3]);
+      }
+    } else if (col < a.cols) {
+#pragma unroll 8
+      for (int64_t q = q0; q < q1; ++q) {
+        const float* src = a.partial + (2 * q + (q == p && rs > p * kEmbedPiece)) * a.cols;
+        // the row's end: columns past it repeat the last one, and are not stored
+        acc.x += src[col]; acc.y += src[col + 1 < a.cols ? col + 1 : col]; acc.z += src[col + 2 < a.cols ? col + 2 : col];
+      }
+    }
+    __syncthreads();   // the run before is stored
+    part[wave][lane] = acc;
+    __syncthreads();
     const int cc = blockIdx.y * 256 + threadIdx.x;
-    if (cc < a.cols) {
-      float* g = a.grad + (int64_t)v * a.cols + cc;
+    if (threadIdx.x < 256 && cc < a.cols) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWaves; ++w) t += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+      const int32_t sl = __builtin_amdgcn_readlane(slot, i);
+      const int64_t v = ((int64_t)(sl % a.per_block) << a.log2nb) + sl / a.per_block;
+      float* g = a.grad + v * a.cols + cc;
       *g = a.accumulate ? __fadd_rn(*g, __fmul_rn(t, a.scale)) : t * a.scale;
     }
   }
 }
 
+// blocks of the sort: one per CU; more where a block would own more rows than its counters hold
+static int embed_log2nb(int64_t rows) {
+  int log2nb = 8;
+  while (((rows + ((int64_t)1 << log2nb) - 1) >> log2nb) > kBinRows) ++log2nb;
+  return log2nb;
+}
+static int64_t embed_per_block(int64_t rows) { return (rows + ((int64_t)1 << embed_log2nb(rows)) - 1) >> embed_log2nb(rows); }
 static int64_t embed_pieces(int64_t n_tokens) { return (n_tokens + kEmbedPiece - 1) / kEmbedPiece; }
 
 size_t embed_bwd_workspace(int64_t rows, int64_t cols, int64_t n_tokens) {
   const int64_t partial = n_tokens > kEmbedPiece ? 2 * embed_pieces(n_tokens) * cols * 4 : 0;
-  return (size_t)(256 + 2 * round_up(rows * 4, 256) + 2 * round_up(n_tokens * 4, 256) + round_up(partial, 256));
+  const int64_t slots = embed_per_block(rows) << embed_log2nb(rows);
+  return (size_t)(256 + 2 * round_up(slots * 4, 256) + 2 * round_up(n_tokens * 4, 256) + round_up(partial, 256));
 }
 
 void embed_bwd_carve(EmbedBwdArgs& a, unsigned char* ws) {
+  a.log2nb = embed_log2nb(a.rows);
+  a.per_block = (int32_t)embed_per_block(a.rows);
+  const int64_t slots = (int64_t)a.per_block << a.log2nb;
   auto take = [&](int64_t bytes) { unsigned char* p = ws; ws += round_up(bytes, 256); return p; };
   a.n_valid = reinterpret_cast<int32_t*>(take(256));
-  a.start = reinterpret_cast<int32_t*>(take(a.rows * 4));
-  a.count = reinterpret_cast<int32_t*>(take(a.rows * 4));
+  a.start = reinterpret_cast<int32_t*>(take(slots * 4));
+  a.count = reinterpret_cast<int32_t*>(take(slots * 4));
   a.order = reinterpret_cast<int32_t*>(take(a.n_tokens * 4));
   a.keys = reinterpret_cast<int32_t*>(take(a.n_tokens * 4));
   a.partial = reinterpret_cast<float*>(ws);
@@ -327,7 +426,7 @@ template <int DD, int CH>
 static void embed_sum_launch(const EmbedBwdArgs& a, hipStream_t s) {
   const int64_t pieces = a.n_tokens > kEmbedPiece ? embed_pieces(a.n_tokens) : 0;
   const int pb = (int)((pieces + 3) / 4);
-  const int64_t items = a.accumulate ? a.n_tokens : a.rows;
+  const int64_t items = (int64_t)((a.per_block + kEmbedGroup - 1) / kEmbedGroup) << a.log2nb;
   const dim3 grid((unsigned)(pb + (items + 3) / 4), (unsigned)((a.cols + 512 * CH - 1) / (512 * CH)));
   if (a.accumulate) hipLaunchKernelGGL((k_embed_sum<DD, CH, true>), grid, dim3(256), 0, s, a, pb);
   else hipLaunchKernelGGL((k_embed_sum<DD, CH, false>), grid, dim3(256), 0, s, a, pb);
@@ -335,9 +434,8 @@ static void embed_sum_launch(const EmbedBwdArgs& a, hipStream_t s) {
 
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dout_dt, hipStream_t s) {
   if (a.n_tokens == 0 && a.accumulate) return hipSuccess;
-  int log2nb = 8;   // a block per CU; more where a block would own more rows than its counters hold
-  while (((a.rows + ((int64_t)1 << log2nb) - 1) >> log2nb) > kBinRows) ++log2nb;
-  hipLaunchKernelGGL(k_embed_bin, dim3(1u << log2nb), dim3(kBinThreads), 0, s, a, log2nb);
+  if (a.wide) hipLaunchKernelGGL((k_embed_bin<true>), dim3(1u << a.log2nb), dim3(kBinThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_embed_bin<false>), dim3(1u << a.log2nb), dim3(kBinThreads), 0, s, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (dout_dt == DT_F32) {
@@ -349,7 +447,8 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dout_dt, hipStream_t s) {
   }
   if ((err = hipGetLastError()) != hipSuccess) return err;
   if (a.n_tokens > kEmbedPiece) {
-    hipLaunchKernelGGL(k_embed_join, dim3((unsigned)embed_pieces(a.n_tokens), (unsigned)((a.cols + 255) / 256)), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(k_embed_join, dim3((unsigned)((embed_pieces(a.n_tokens) + kJoinPieces - 1) / kJoinPieces), (unsigned)((a.cols + 255) / 256)),
+                       dim3(kJoinWaves * 64), 0, s, a);
     err = hipGetLastError();
   }
   return err;

@@ -13,7 +13,8 @@
 
 namespace ma {
 
-constexpr int norm_threads(int G) { return G < 256 ? 256 : G; }
+// threads of a block: a wave per row takes 4 rows, more lanes per row one row
+constexpr int norm_threads(int G) { return G == 64 ? 256 : G; }
 
 // Sums over the G lanes of a row's group, the same in every lane: within the
 // wave, then over the group's waves through `part` (the group's own; each
@@ -22,7 +23,7 @@ constexpr int norm_threads(int G) { return G < 256 ? 256 : G; }
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[16]) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+  for (int n = 0; n < N; ++n) v[n] = wave_sum_dpp(v[n]);
   if constexpr (G > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -39,12 +40,12 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[16]) {
   }
 }
 
-template <int XD, int YD, int G, int CH>
+template <int XD, int YD, int G, int CH, bool NT>
 __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs a) {
   constexpr int ROWS = norm_threads(G) / G;
   __shared__ float part[2][2][1][16];
   const int t = threadIdx.x % G;
-  const float n = (float)a.cols;
+  const float per = 1.0f / (float)a.cols;
   int flip = 0;
   for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / G; row < a.rows; row += (int64_t)gridDim.x * ROWS, flip ^= 1) {
     const unsigned char* src = elem_ptr<XD>(a.x, row * a.cols);
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
         raw[c] = col < a.cols ? raw_load_row<XD>(src, col, a.cols) : raw_zero<XD>();
       }
 #pragma unroll
-      for (int c = 0; c < CH; ++c) raw_f32<XD>(raw[c], x[c]);
+      for (int c = 0; c < CH; ++c) raw_f32_row<XD>(raw[c], (c * G + t) * 8, a.cols, x[c]);
     }
     float s[1] = {0.0f};
 #pragma unroll
@@ -65,17 +66,27 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[0] += x[c][e];
     group_sum<G>(s, part[flip][0]);
-    const float mean = s[0] / n;
+    const float mean = s[0] * per;
     float q[1] = {0.0f};
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+      const int in = a.cols - (c * G + t) * 8;
+      if (in >= 8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = (c * G + t) * 8 + e < a.cols ? x[c][e] - mean : 0.0f;
-        q[0] = __builtin_fmaf(d, d, q[0]);
+        for (int e = 0; e < 8; ++e) {
+          const float d = x[c][e] - mean;
+          q[0] = __builtin_fmaf(d, d, q[0]);
+        }
+      } else if (in > 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = e < in ? x[c][e] - mean : 0.0f;
+          q[0] = __builtin_fmaf(d, d, q[0]);
+        }
       }
+    }
     group_sum<G>(q, part[flip][1]);
-    const float rstd = 1.0f / __fsqrt_rn(q[0] / n + a.eps);
+    const float rstd = rsqrtf(__builtin_fmaf(q[0], per, a.eps));
     if (t == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
     unsigned char* dst = elem_ptr<YD>(a.y, row * a.cols);
 #pragma unroll
@@ -86,23 +97,23 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = (x[c][e] - mean) * rstd;
       if (a.gain) {
-        raw_f32<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols), w);
+        raw_f32_row<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols), col, a.cols, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] *= w[e];
       }
       if (a.bias) {
-        raw_f32<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.bias, 0), col, a.cols), b);
+        raw_f32_row<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.bias, 0), col, a.cols), col, a.cols, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] += b[e];
       }
-      store_row<YD>(dst, col, a.cols, y);
+      store_row<YD, NT>(dst, col, a.cols, y);
     }
     if (a.q) {
       const int64_t pitch = act_pitch(a.cols);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = (c * G + t) * 8;
-        const int e = act_exponent(act_block_amax(x[c]));
+        const int e = act_block_exponent(x[c]);
         if (col >= pitch) continue;
         *reinterpret_cast<uint2*>(a.q + row * pitch + col) = act_encode(x[c], e);
         if (t % 16 == 0) a.qscale[row * (pitch / kActBlock) + col / kActBlock] = (uint8_t)(e + 127);
@@ -122,7 +133,7 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
   __shared__ float part[2][2][16];
   __shared__ float join[G == 64 ? 512 * CH : 1];
   const int t = threadIdx.x % G, group = threadIdx.x / G;
-  const float n = (float)a.cols;
+  const float per = 1.0f / (float)a.cols;
   const int64_t pitch = act_pitch(a.cols);
   const int64_t units = (a.rows + ROWS - 1) / ROWS, share = (units + a.blocks - 1) / a.blocks;
   const int64_t u0 = blockIdx.x * share, u1 = u0 + share < units ? u0 + share : units;
@@ -131,56 +142,112 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[c][e] = db[c][e] = 0.0f;
+  // a row's operands, loaded while the row before it is computed; x comes from a
+  // forward pass long ago and is not read again soon (non-temporal), dy is fresh
+  constexpr int XR = raw_dt<XD>();
+  struct Row {
+    Raw8<XR> x[CH];
+    uint2 q[CH];
+    uint32_t sc[CH];
+    Raw8<DYD> dy[CH];
+    float2 st;
+  };
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+    Row r;
+    if (row >= a.rows) return r;
+    r.st = *reinterpret_cast<const float2*>(a.stats + 2 * row);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = (c * G + t) * 8;
+      if (col >= a.cols) continue;
+      if constexpr (XD == DT_ACT8) {
+        r.q[c] = ld8_nt(a.q + row * pitch + col);
+        r.sc[c] = a.qscale[row * (pitch / kActBlock) + col / kActBlock];
+      } else {
+        r.x[c] = raw_load_row<XR, true>(elem_ptr<XR>(a.x, row * a.cols), col, a.cols);
+      }
+      r.dy[c] = raw_load_row<DYD>(elem_ptr<DYD>(a.dy, row * a.cols), col, a.cols);
+    }
+    return r;
+  };
+  // where the registers are there: the row ahead, and xh and g kept over the reduction (else they are read again, from L2)
+  constexpr bool AHEAD = G * CH < 2048, HOLD = G * CH < 2048;
+  float w0[8];   // the gain, kept where a lane has one chunk only
+  if (CH == 1 && a.gain && t * 8 < a.cols)
+    raw_f32_row<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), t * 8, a.cols), t * 8, a.cols, w0);
+  Row next = load(AHEAD && u0 < u1 ? u0 * ROWS + group : a.rows);
   int flip = 0;
   for (int64_t u = u0; u < u1; ++u, flip ^= 1) {
     const int64_t row = u * ROWS + group;
     if (G == 64 && row >= a.rows) break;
-    float xh[CH][8], g[CH][8];
+    const Row now = AHEAD ? next : load(row);
+    if constexpr (AHEAD) next = load(u + 1 < u1 ? row + ROWS : a.rows);
     float s[2] = {0.0f, 0.0f};
-    const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * row);
+    const float2 st = now.st;
+    // xh and dy of chunk c (zeros past the row's end, whatever the row's factors are), and the gain
+    auto chunk = [&](const Row& r, int c, float (&xh)[8], float (&d)[8], float (&w)[8]) __attribute__((always_inline)) {
+      const int col = (c * G + t) * 8;
+      if constexpr (XD == DT_ACT8) act_decode(r.q[c], act_scale(r.sc[c]), xh);
+      else raw_f32_row<XR>(r.x[c], col, a.cols, xh);
+      raw_f32_row<DYD>(r.dy[c], col, a.cols, d);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xh[e] = (xh[e] - st.x) * st.y;
+      if ((a.cols & 7) && col + 8 > a.cols) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + e >= a.cols) xh[e] = 0.0f;
+      }
+      if (a.gain) {
+        if constexpr (CH == 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = w0[e];
+        } else {
+          raw_f32_row<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols), col, a.cols, w);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+      }
+    };
+    float xh[HOLD ? CH : 1][8], g[HOLD ? CH : 1][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * G + t) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xh[c][e] = g[c][e] = 0.0f;
-      if (col >= a.cols) continue;
-      if constexpr (XD == DT_ACT8) {
-        const float sc = act_scale(a.qscale[row * (pitch / kActBlock) + col / kActBlock]);
-        act_decode(*reinterpret_cast<const uint2*>(a.q + row * pitch + col), sc, xh[c]);
-      } else {
-        raw_f32<raw_dt<XD>()>(raw_load_row<raw_dt<XD>()>(elem_ptr<raw_dt<XD>()>(a.x, row * a.cols), col, a.cols), xh[c]);
-      }
-      raw_f32<DYD>(raw_load_row<DYD>(elem_ptr<DYD>(a.dy, row * a.cols), col, a.cols), g[c]);
-      float w[8];
-      if (a.gain) raw_f32<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols), w);
+      float(&x)[8] = xh[HOLD ? c : 0], (&d)[8] = g[HOLD ? c : 0], w[8];
+      if ((c * G + t) * 8 >= a.cols) continue;
+      chunk(now, c, x, d, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[c][e] = (xh[c][e] - st.x) * st.y;
-        if (col + e >= a.cols) xh[c][e] = 0.0f;   // its dy is zero, but a NaN or infinite factor would not be
-        dg[c][e] = __builtin_fmaf(g[c][e], xh[c][e], dg[c][e]);
-        db[c][e] += g[c][e];
-        if (a.gain) g[c][e] *= w[e];
-        s[0] += g[c][e];
-        s[1] = __builtin_fmaf(g[c][e], xh[c][e], s[1]);
+        dg[c][e] = __builtin_fmaf(d[e], x[e], dg[c][e]);
+        db[c][e] += d[e];
+        d[e] *= w[e];
+        s[0] += d[e];
+        s[1] = __builtin_fmaf(d[e], x[e], s[1]);
       }
     }
     group_sum<G>(s, part[flip]);
-    const float m0 = s[0] / n, m1 = s[1] / n;
+    const float m0 = s[0] * per, m1 = s[1] * per;
+    const Row again = HOLD ? Row() : load(row);
     unsigned char* dst = elem_ptr<DXD>(a.dx, row * a.cols);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * G + t) * 8;
       if (col >= a.cols) continue;
-      float d[8];
+      float(&x)[8] = xh[HOLD ? c : 0], (&d)[8] = g[HOLD ? c : 0], w[8], out[8];
+      if constexpr (!HOLD) {
+        chunk(again, c, x, d, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = st.y * (g[c][e] - m0 - xh[c][e] * m1);
-      store_row<DXD>(dst, col, a.cols, d);
+        for (int e = 0; e < 8; ++e) d[e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = st.y * (d[e] - m0 - x[e] * m1);
+      store_row<DXD>(dst, col, a.cols, out);
     }
   }
   if (!a.partial) return;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float* out = a.partial + ((int64_t)blockIdx.x * 2 + which) * a.cols;
+    // by 32 columns, so that k_norm_cols reads one contiguous stretch
+    float* const out = a.partial + (int64_t)which * round_up(a.cols, 32) * a.blocks;
     float(&v)[CH][8] = which ? db : dg;
     if constexpr (G == 64) {
       // the block's rows in order of their wave
@@ -201,54 +268,68 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * G + t) * 8;
-      if (col < a.cols) store_row<DT_F32>(reinterpret_cast<unsigned char*>(out), col, a.cols, v[c]);
+      if (col < a.cols) {
+        float4* p = reinterpret_cast<float4*>(out + ((int64_t)(col / 32) * a.blocks + blockIdx.x) * 32 + col % 32);
+        p[0] = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+        p[1] = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+      }
     }
   }
 }
 
-// dgain (y = 0) and dbias (y = 1): 64 columns per block, its 16 waves summing
-// 16 contiguous shares of the blocks' sums, then those in order.
+// dgain (y = 0) and dbias (y = 1): 32 columns per block, 32 groups of lanes
+// summing as many contiguous shares of the blocks' sums, then those in order.
 __global__ void __launch_bounds__(1024) k_norm_cols(const NormBwdArgs a) {
-  __shared__ float part[16][64];
+  __shared__ float part[32][32];
   float* out = blockIdx.y ? a.dbias : a.dgain;
   if (!out) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
-  const int share = (a.blocks + 15) / 16, b0 = wave * share, b1 = b0 + share < a.blocks ? b0 + share : a.blocks;
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  const int share = (a.blocks + 31) / 32, b0 = group * share, b1 = b0 + share < a.blocks ? b0 + share : a.blocks;
   float v = 0.0f;
-  if (col < a.cols) {
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b) v += a.partial[((int64_t)b * 2 + blockIdx.y) * a.cols + col];
-  }
-  part[wave][lane] = v;
+  const float* src = a.partial + (int64_t)blockIdx.y * round_up(a.cols, 32) * a.blocks + (int64_t)blockIdx.x * a.blocks * 32 + lane;
+#pragma unroll 16
+  for (int b = b0; b < b1; ++b) v += src[b * 32];
+  part[group][lane] = v;
   __syncthreads();
-  if (wave == 0 && col < a.cols) {
+  if (group == 0 && col < a.cols) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t += part[w][lane];
+    for (int w = 0; w < 32; ++w) t += part[w][lane];
     out[col] = a.accumulate ? __fadd_rn(out[col], t) : t;
   }
 }
 
-// Lanes and chunks per row by its length: f(G, CH) as integral constants.
+// Lanes and chunks per row by its length: f(NormShape<G, CH>).
 template <int G_, int CH_> struct NormShape { static constexpr int G = G_, CH = CH_; };
 template <typename F>
-static hipError_t norm_shape(int64_t cols, F&& f) {
+static hipError_t norm_fwd_shape(int64_t cols, F&& f) {
   if (cols <= 512) return f(NormShape<64, 1>());
   if (cols <= 1024) return f(NormShape<64, 2>());
-  if (cols <= 2048) return f(NormShape<256, 1>());
+  if (cols <= 2048) return f(NormShape<128, 2>());
   if (cols <= 4096) return f(NormShape<256, 2>());
   if (cols <= 8192) return f(NormShape<1024, 1>());
   return f(NormShape<1024, 2>());   // kMaxNormCols
 }
-static int norm_rows_per_block(int64_t cols) { return cols <= 1024 ? 4 : 1; }
+template <typename F>
+static hipError_t norm_bwd_shape(int64_t cols, F&& f) {
+  if (cols <= 512) return f(NormShape<64, 1>());
+  if (cols <= 1024) return f(NormShape<64, 2>());
+  if (cols <= 2048) return f(NormShape<256, 1>());
+  if (cols <= 4096) return f(NormShape<512, 1>());
+  if (cols <= 8192) return f(NormShape<1024, 1>());
+  return f(NormShape<1024, 2>());
+}
 
 template <int XD, int YD>
 static hipError_t norm_fwd(const NormFwdArgs& a, hipStream_t s) {
-  return norm_shape(a.cols, [&](auto sh) {
+  return norm_fwd_shape(a.cols, [&](auto sh) {
     constexpr int G = decltype(sh)::G, CH = decltype(sh)::CH;
     const int64_t per = norm_threads(G) / G, want = (a.rows + per - 1) / per, most = (int64_t)1 << 21;
-    hipLaunchKernelGGL((k_norm_fwd<XD, YD, G, CH>), dim3((unsigned)(want < most ? want : most)), dim3(norm_threads(G)), 0, s, a);
+    const dim3 grid((unsigned)(want < most ? want : most)), block(norm_threads(G));
+    const int64_t bytes = a.rows * a.cols * (elem_bytes<XD>() + elem_bytes<YD>() + (a.q ? 1 : 0));
+    if (bytes > kStreamBytes) hipLaunchKernelGGL((k_norm_fwd<XD, YD, G, CH, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_norm_fwd<XD, YD, G, CH, false>), grid, block, 0, s, a);
     return hipGetLastError();
   });
 }
@@ -259,15 +340,21 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dt, int y_dt, hipStream_t
   return y_dt == DT_F32 ? norm_fwd<DT_BF16, DT_F32>(a, s) : norm_fwd<DT_BF16, DT_BF16>(a, s);
 }
 
+// as many as are resident at once: 16 waves per CU
 int norm_bwd_blocks(int64_t rows, int64_t cols) {
-  const int64_t per = norm_rows_per_block(cols), units = (rows + per - 1) / per;
-  const int64_t most = cols <= 4096 ? 1024 : 512;
+  int64_t units = rows, most = 0;
+  (void)norm_bwd_shape(cols, [&](auto sh) {
+    constexpr int G = decltype(sh)::G;
+    units = (rows + norm_threads(G) / G - 1) / (norm_threads(G) / G);
+    most = 256 * 16 * 64 / norm_threads(G);
+    return hipSuccess;
+  });
   return (int)(units < most ? units : most);
 }
 
 template <int XD, int DYD, int DXD>
 static hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
-  return norm_shape(a.cols, [&](auto sh) {
+  return norm_bwd_shape(a.cols, [&](auto sh) {
     constexpr int G = decltype(sh)::G, CH = decltype(sh)::CH;
     hipLaunchKernelGGL((k_norm_bwd<XD, DYD, DXD, G, CH>), dim3((unsigned)a.blocks), dim3(norm_threads(G)), 0, s, a);
     return hipGetLastError();
@@ -283,7 +370,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dt, int dy_dt, int dx_dt,
     else err = dy_dt == DT_F32 ? norm_bwd<DT_BF16, DT_F32, DT_BF16>(a, s) : norm_bwd<DT_BF16, DT_BF16, DT_BF16>(a, s);
   }
   if (err != hipSuccess || (!a.dgain && !a.dbias)) return err;
-  hipLaunchKernelGGL(k_norm_cols, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(1024), 0, s, a);
+  hipLaunchKernelGGL(k_norm_cols, dim3((unsigned)((a.cols + 31) / 32), 2), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

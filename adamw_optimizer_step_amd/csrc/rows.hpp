@@ -6,6 +6,15 @@
 
 namespace ma {
 
+// Calls whose operands together exceed this do not fit the 256 MB memory-side
+// cache beside anything else: they mark the larger of what they pass through as
+// non-temporal, so that it does not push out what the rest of the call, or the
+// next one, can still find there. Below it they leave the cache to the next
+// call. (Layer norm of 24576 x 2048 bf16 with its checkpoint, 252 MB: 45 us with
+// y stored non-temporally, 59 us without; of 32768 x 1024, 134 MB: 29 us both
+// ways, and a pass over y after it 22 us against 19.5.)
+constexpr int64_t kStreamBytes = (int64_t)192 << 20;
+
 // A 16-byte access at 2- or 4-byte alignment: gfx950 serves it as one
 // global_load_dwordx4 / global_store_dwordx4 whatever the address, so a row
 // that starts anywhere (odd column counts, views) takes the same path as an
@@ -24,8 +33,18 @@ __device__ __forceinline__ unsigned char* elem_ptr(void* base, int64_t i) {
 }
 
 // The raw 8 elements at p (16 bytes of bf16, 32 of fp32), converted later, so
-// that several loads can be in flight at a low register cost.
+// that several loads can be in flight at a low register cost. NT (non-temporal)
+// holds for bf16, where a wave's access covers whole cache lines; the two halves
+// of an fp32 access meet in the cache (zeros written through it 5.9 TB/s, past
+// it 2.2 TB/s).
 template <int DT> struct Raw8 { u32x4_t u[DT == DT_BF16 ? 1 : 2]; };
+
+// 8 bytes, optionally non-temporal (see kStreamBytes)
+typedef uint32_t u32x2_nt_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint2 ld8_nt(const void* p) {
+  const u32x2_nt_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x2_nt_t*>(p));
+  return make_uint2(x[0], x[1]);
+}
 
 template <int DT>
 __device__ __forceinline__ Raw8<DT> raw_zero() {
@@ -43,26 +62,88 @@ __device__ __forceinline__ Raw8<DT> raw_load(const unsigned char* p) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const V* q = reinterpret_cast<const V*>(p) + i;
-    if constexpr (NT) r.u[i] = __builtin_nontemporal_load(q);
+    if constexpr (NT && DT == DT_BF16) r.u[i] = __builtin_nontemporal_load(q);
     else r.u[i] = *q;
   }
   return r;
 }
 
-// Elements col .. col+7 of a row of `cols` elements at `row`; zeros past its end.
+// Elements col .. col+7 (col < cols) of a row of `cols` elements at `row`. The
+// row's last, partial group loads the row's last 8 elements instead, whole and
+// inside the row; raw_f32_row (or raw_fix) moves them to their places. Rows of
+// fewer than 8 elements are put together one by one.
 template <int DT, bool NT = false>
 __device__ __forceinline__ Raw8<DT> raw_load_row(const unsigned char* row, int col, int cols) {
-  const unsigned char* p = row + (int64_t)col * elem_bytes<DT>();
-  if (col + 8 <= cols) return raw_load<DT, NT>(p);
+  if (cols >= 8) return raw_load<DT, NT>(row + (int64_t)(col + 8 <= cols ? col : cols - 8) * elem_bytes<DT>());
   Raw8<DT> r = raw_zero<DT>();
+#pragma unroll 1
+  for (int k = cols - 1; k >= 0; --k) {
+    if constexpr (DT == DT_BF16) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (col + i < cols) {
-      if constexpr (DT == DT_BF16) r.u[0][i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-      else r.u[i / 4][i % 4] = reinterpret_cast<const uint32_t*>(p)[i];
+      for (int i = 3; i > 0; --i) r.u[0][i] = r.u[0][i] << 16 | r.u[0][i - 1] >> 16;
+      r.u[0][0] = r.u[0][0] << 16 | reinterpret_cast<const uint16_t*>(row)[k];
+    } else {
+#pragma unroll
+      for (int i = 7; i > 0; --i) r.u[i / 4][i % 4] = r.u[(i - 1) / 4][(i - 1) % 4];
+      r.u[0][0] = reinterpret_cast<const uint32_t*>(row)[k];
     }
   }
   return r;
+}
+
+// What raw_load_row(row, col, cols) loaded, with every element in its place and
+// zeros past the row's end.
+template <int DT>
+__device__ __forceinline__ void raw_fix(Raw8<DT>& r, int col, int cols) {
+  if ((cols & 7) == 0) return;     // (the same for every lane: no row has a partial group)
+  const int by = col + 8 - cols;   // elements too far up
+  if (by <= 0 || cols < 8) return;
+  constexpr int W = DT == DT_BF16 ? 4 : 8;   // 32-bit words, 2 or 1 elements each
+  uint32_t w[W + 4] = {};
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = r.u[i / 4][i % 4];
+  constexpr int E = DT == DT_BF16 ? 2 : 1;
+#pragma unroll
+  for (int step = 4; step >= E; step /= 2) {
+    if (by & step) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = w[i + step / E];
+    }
+  }
+  if constexpr (DT == DT_BF16) {
+    if (by & 1) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = w[i] >> 16 | w[i + 1] << 16;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) r.u[i / 4][i % 4] = w[i];
+}
+
+// ----------------------------------------------------------------------------
+// Reductions across lanes by DPP moves: no LDS round trips. Lane exchanges
+// within 16 lanes: neighbours, pairs, halves mirrored, the row mirrored.
+// ----------------------------------------------------------------------------
+template <int CTRL, typename T>
+__device__ __forceinline__ T dpp(T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+constexpr int kDppNeighbour = 0xB1, kDppPair = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+template <typename T, typename F>
+__device__ __forceinline__ T reduce16(T x, F&& f) {
+  x = f(x, dpp<kDppNeighbour>(x));
+  x = f(x, dpp<kDppPair>(x));
+  x = f(x, dpp<kDppHalfMirror>(x));
+  return f(x, dpp<kDppMirror>(x));
+}
+
+// The wave's sum, the same in every lane.
+__device__ __forceinline__ float wave_sum_dpp(float x) {
+  x = reduce16(x, [](float a, float b) { return a + b; });
+  const float a = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 0)), b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 16));
+  const float c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 32)), d = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 48));
+  return (a + b) + (c + d);
 }
 
 template <int DT>
@@ -72,6 +153,12 @@ __device__ __forceinline__ void raw_f32(const Raw8<DT>& r, float (&v)[8]) {
     if constexpr (DT == DT_BF16) v[i] = __uint_as_float(i & 1 ? r.u[0][i / 2] & 0xFFFF0000u : r.u[0][i / 2] << 16);
     else v[i] = __uint_as_float(r.u[i / 4][i % 4]);
   }
+}
+
+template <int DT>
+__device__ __forceinline__ void raw_f32_row(Raw8<DT> r, int col, int cols, float (&v)[8]) {
+  raw_fix<DT>(r, col, cols);
+  raw_f32<DT>(r, v);
 }
 
 // v to elements col .. col+7 of the row (those inside it), rounded once.
@@ -90,7 +177,7 @@ __device__ __forceinline__ void store_row(unsigned char* row, int col, int cols,
     constexpr int N = DT == DT_BF16 ? 1 : 2;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if constexpr (NT) __builtin_nontemporal_store((V)u[i], reinterpret_cast<V*>(p) + i);
+      if constexpr (NT && DT == DT_BF16) __builtin_nontemporal_store((V)u[i], reinterpret_cast<V*>(p) + i);
       else reinterpret_cast<V*>(p)[i] = u[i];
     }
     return;
@@ -126,22 +213,44 @@ __device__ __forceinline__ int act_exponent(float amax) {
 
 __device__ __forceinline__ float act_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// |x| where it counts towards amax
-__device__ __forceinline__ float act_mag(float x) {
-  const float a = __builtin_fabsf(x);
-  return a < __builtin_inff() ? a : 0.0f;
-}
-
-// 8 values over 2^e as e4m3 bytes
-__device__ __forceinline__ uint2 act_encode(const float (&v)[8], int e) {
-  const float inv = act_pow2(-e);
-  const float most = e == kActEmax ? 240.0f : 448.0f;
-  float t[8];
+// The exponent of the block that the 16 lanes 16j .. 16j+15 hold, 8 columns
+// each. Magnitudes are compared as their bits, where infinities and NaN stand
+// above every finite value: a block without any is done in one pass, another
+// goes over its values again without them.
+__device__ __forceinline__ int act_block_exponent(const float (&v)[8]) {
+  constexpr uint32_t kInf = 0x7F800000u;
+  auto over = [](uint32_t a) __attribute__((always_inline)) { return reduce16(a, [](uint32_t x, uint32_t y) { return x > y ? x : y; }); };
+  uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = v[i] * inv;
-    // finite values are within `most`, but for those of the largest exponent
-    t[i] = act_mag(v[i]) == __builtin_fabsf(v[i]) ? __builtin_fminf(__builtin_fmaxf(x, -most), most) : __builtin_nanf("");
+    const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    a = a > m ? a : m;
+  }
+  a = over(a);
+  if (__any(a >= kInf)) {
+    a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+      a = m < kInf && m > a ? m : a;
+    }
+    a = over(a);
+  }
+  return act_exponent(__uint_as_float(a));
+}
+
+// 8 values over 2^e as e4m3 bytes. Every finite value is within 448 * 2^e but
+// for those of the largest exponent; NaN and what exceeds the range, here the
+// infinities, become NaN.
+__device__ __forceinline__ uint2 act_encode(const float (&v)[8], int e) {
+  const float inv = act_pow2(-e);
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
+  if (e == kActEmax) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (__builtin_fabsf(t[i]) < __builtin_inff()) t[i] = __builtin_fminf(__builtin_fmaxf(t[i], -240.0f), 240.0f);
   }
   uint32_t lo = 0, hi = 0;
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], lo, false);
@@ -151,24 +260,20 @@ __device__ __forceinline__ uint2 act_encode(const float (&v)[8], int e) {
   return make_uint2(lo, hi);
 }
 
+__device__ __forceinline__ float act_scale(uint32_t b) { return __uint_as_float(b << 23); }
+
 // 8 e4m3 bytes times s (a power of two)
 __device__ __forceinline__ void act_decode(uint2 q, float s, float (&v)[8]) {
-  const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(q.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q.x, true);
-  const f32x2_t c = __builtin_amdgcn_cvt_pk_f32_fp8(q.y, false), d = __builtin_amdgcn_cvt_pk_f32_fp8(q.y, true);
-  v[0] = a[0] * s; v[1] = a[1] * s; v[2] = b[0] * s; v[3] = b[1] * s;
-  v[4] = c[0] * s; v[5] = c[1] * s; v[6] = d[0] * s; v[7] = d[1] * s;
+  const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.x, s, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.x, s, true);
+  const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.y, s, false), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.y, s, true);
+  v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
+  v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
 }
 
-__device__ __forceinline__ float act_scale(uint8_t b) { return __uint_as_float((uint32_t)b << 23); }
-
-// amax over the 16 lanes that hold one block (lanes 16j .. 16j+15, 8 columns each)
-__device__ __forceinline__ float act_block_amax(const float (&v)[8]) {
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = __builtin_fmaxf(a, act_mag(v[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = __builtin_fmaxf(a, __shfl_xor(a, o, kWave));
-  return a;
+// 4 e4m3 bytes times s as packed bf16, exact
+__device__ __forceinline__ uint2 act_decode_bf16(uint32_t q, float s) {
+  return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, false)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, true)));
 }
 
 }  // namespace ma

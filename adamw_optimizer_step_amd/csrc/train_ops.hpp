@@ -21,7 +21,7 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hip
 
 // Runs of the sorted tokens longer than this are summed in pieces of as many
 // sorted positions, one wave each, and joined in order.
-constexpr int kEmbedPiece = 64;
+constexpr int kEmbedPiece = 32;
 struct EmbedBwdArgs {
   const void* dout;
   const void* tokens;
@@ -29,11 +29,12 @@ struct EmbedBwdArgs {
   int64_t rows, n_tokens;
   int32_t cols, wide, accumulate;
   float scale;
-  // workspace: start / count of every row's run in the sorted order, the
-  // positions and rows in that order, the number of valid tokens, and two
-  // partial rows for each piece
+  // workspace: the number of valid tokens, start / count of every row's run in
+  // the sorted order (by slot, see k_embed_bin), the positions and slots in that
+  // order, and two partial rows for each piece
   int32_t *n_valid, *start, *count, *order, *keys;
   float* partial;
+  int32_t log2nb, per_block;   // the sort's blocks (2^log2nb) and rows per block
 };
 size_t embed_bwd_workspace(int64_t rows, int64_t cols, int64_t n_tokens);
 void embed_bwd_carve(EmbedBwdArgs& a, unsigned char* ws);
@@ -60,7 +61,7 @@ struct NormBwdArgs {
   const float *stats, *gain;
   void* dx;
   float *dgain, *dbias;       // either may be null
-  float* partial;             // [blocks][2][cols]
+  float* partial;             // [2][cols / 32][blocks][32]
   int64_t rows;
   int32_t cols, accumulate, blocks;
 };
