@@ -10,7 +10,6 @@ that are not passed in are allocated for that stream. Names follow the C ABI
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from typing import Optional, Tuple, Union
 
@@ -20,7 +19,6 @@ from . import _lib as L
 from .api import _DT, _dt
 
 _TOKENS = {torch.int32: 4, torch.int64: 8}
-_HERE = contextlib.nullcontext()
 
 
 def _check(what: str, t: torch.Tensor, dtypes, shape=None) -> torch.Tensor:
@@ -55,30 +53,20 @@ def _device(*tensors: Optional[torch.Tensor]) -> torch.device:
     return dev
 
 
-class _Launch:
-    """The device and stream of a call: makes the tensors' device current, and
-    the call's stream too where one is given, so that what is allocated inside
-    belongs to it."""
-
-    __slots__ = ("dev", "stream", "ctx")
-
-    def __init__(self, dev: torch.device, stream):
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.dev, self.stream = dev, stream
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)   # makes its device current too
-        else:
-            self.ctx = _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        self.ctx.__enter__()
-        return (self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)).cuda_stream
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+def _launch(dev: torch.device, stream, go):
+    """``go(raw stream)`` with the tensors' device current and, where a stream is
+    given, that stream too, so that what ``go`` allocates belongs to it."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return go(torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.device(dev):
+            return go(torch._C._cuda_getCurrentRawStream(dev.index))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):   # makes its device current too
+        return go(stream.cuda_stream)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -114,12 +102,15 @@ def embedding_forward(table: torch.Tensor, tokens: torch.Tensor, scale: float = 
     elif dtype is not None and dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     dev = _device(table, tokens, out)
-    with _Launch(dev, stream) as s:
+
+    def go(s):
+        nonlocal out
         if out is None:
             out = torch.empty(shape, dtype=dtype or table.dtype, device=dev)
         L.check(L.lib().ma_embedding_forward(table.data_ptr(), _dt(table), rows, cols, tokens.data_ptr(), _TOKENS[tokens.dtype],
                                              tokens.numel(), scale, out.data_ptr(), _dt(out), s))
-    return out
+        return out
+    return _launch(dev, stream, go)
 
 
 def embedding_workspace_size(rows: int, cols: int, n_tokens: int) -> int:
@@ -146,11 +137,13 @@ def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, grad: torch.Ten
     _check_workspace(workspace)
     n = tokens.numel()
     dev = _device(dout, tokens, grad, workspace)
-    with _Launch(dev, stream) as s:
+
+    def go(s):
         ws = _workspace(workspace, embedding_workspace_size(rows, cols, n), dev)
         L.check(L.lib().ma_embedding_backward(dout.data_ptr(), _dt(dout), tokens.data_ptr(), _TOKENS[tokens.dtype], n, rows, cols,
                                               scale, int(bool(accumulate)), grad.data_ptr(), ws.data_ptr(), ws.numel(), s))
-    return grad
+        return grad
+    return _launch(dev, stream, go)
 
 
 # ---------------------------------------------------------------------------
@@ -175,9 +168,14 @@ class ActCheckpoint:
     @classmethod
     def empty(cls, rows: int, cols: int, device) -> "ActCheckpoint":
         """Room for the checkpoint of a ``[rows, cols]`` matrix."""
+        if rows < 0 or cols < 1:
+            raise ValueError(f"no checkpoint of {rows} rows and {cols} columns")
         blocks = -(-cols // L.MA_ACT_BLOCK)
-        return cls(torch.empty((rows, blocks * L.MA_ACT_BLOCK), dtype=torch.uint8, device=device),
-                   torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols)
+        self = cls.__new__(cls)
+        self.q = torch.empty((rows, blocks * L.MA_ACT_BLOCK), dtype=torch.uint8, device=device)
+        self.scale = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+        self.rows, self.cols = rows, cols
+        return self
 
     def nbytes(self) -> int:
         return self.q.numel() + self.scale.numel()
@@ -199,11 +197,14 @@ def act_pack(x: torch.Tensor, out: Optional[ActCheckpoint] = None, stream=None) 
     if out is not None:
         _check_checkpoint("out", out, rows, cols)
     dev = _device(x, out.q, out.scale) if out is not None else _device(x)
-    with _Launch(dev, stream) as s:
+
+    def go(s):
+        nonlocal out
         if out is None:
             out = ActCheckpoint.empty(rows, cols, dev)
         L.check(L.lib().ma_act_pack(x.data_ptr(), _dt(x), rows, cols, out.q.data_ptr(), out.scale.data_ptr(), s))
-    return out
+        return out
+    return _launch(dev, stream, go)
 
 
 def act_unpack(checkpoint: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
@@ -220,11 +221,14 @@ def act_unpack(checkpoint: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, o
     elif dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     dev = _device(checkpoint.q, checkpoint.scale, out)
-    with _Launch(dev, stream) as s:
+
+    def go(s):
+        nonlocal out
         if out is None:
             out = torch.empty((rows, cols), dtype=dtype, device=dev)
         L.check(L.lib().ma_act_unpack(checkpoint.q.data_ptr(), checkpoint.scale.data_ptr(), rows, cols, out.data_ptr(), _dt(out), s))
-    return out
+        return out
+    return _launch(dev, stream, go)
 
 
 # ---------------------------------------------------------------------------
@@ -257,14 +261,17 @@ def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias
     if checkpoint is not None:
         q, sc = _check_checkpoint("checkpoint", checkpoint, rows, cols).q, checkpoint.scale
     dev = _device(x, gain, bias, out, stats, q, sc)
-    with _Launch(dev, stream) as s:
+
+    def go(s):
+        nonlocal out, stats
         if out is None:
             out = torch.empty(x.shape, dtype=dtype or x.dtype, device=dev)
         if stats is None:
             stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
         L.check(L.lib().ma_layernorm_forward(x.data_ptr(), _dt(x), rows, cols, _ptr(gain), _ptr(bias), eps, out.data_ptr(), _dt(out),
                                              stats.data_ptr(), _ptr(q), _ptr(sc), s))
-    return out, stats
+        return out, stats
+    return _launch(dev, stream, go)
 
 
 def layernorm_workspace_size(rows: int, cols: int) -> int:
@@ -300,14 +307,17 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
     _check_workspace(workspace)
     dev = _device(dy, xt, q, sc, stats, gain, dgain, dbias, dx, workspace)
     sums = dgain is not None or dbias is not None
-    with _Launch(dev, stream) as s:
+
+    def go(s):
+        nonlocal dx
         if dx is None:
             dx = torch.empty(dy.shape, dtype=dx_dtype, device=dev)
         ws = _workspace(workspace, layernorm_workspace_size(rows, cols), dev) if sums else None
         L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, _ptr(q), _ptr(sc), rows, cols, stats.data_ptr(),
                                               _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
                                               _ptr(ws), ws.numel() if sums else 0, s))
-    return dx
+        return dx
+    return _launch(dev, stream, go)
 
 
 # ---------------------------------------------------------------------------
@@ -338,9 +348,11 @@ def act_weight_grad(dy: torch.Tensor, x: ActCheckpoint, grad: torch.Tensor, accu
     _check("grad", grad, _DT, (outs, x.cols))
     _check_workspace(workspace)
     dev = _device(dy, x.q, x.scale, grad, workspace)
-    with _Launch(dev, stream) as s:
+
+    def go(s):
         need = act_weight_grad_workspace_size(tokens, outs, x.cols, dy.dtype)
         ws = _workspace(workspace, need, dev) if need or workspace is not None else None
         L.check(L.lib().ma_act_weight_grad(dy.data_ptr(), _dt(dy), x.q.data_ptr(), x.scale.data_ptr(), tokens, outs, x.cols,
                                            grad.data_ptr(), _dt(grad), int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0, s))
-    return grad
+        return grad
+    return _launch(dev, stream, go)
