@@ -245,8 +245,8 @@ int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
 
 static int wgrad_sizes(const char* fn, int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype) {
   int rc;
-  if ((rc = check_size(fn, "tokens", tokens, 0, kMaxTokens)) || (rc = check_size(fn, "outs", outs, 1, kMaxCols)) ||
-      (rc = check_size(fn, "ins", ins, 1, kMaxCols)) || (rc = check_dtype(fn, "dy", dy_dtype)))
+  if ((rc = check_size(fn, "tokens", tokens, 0, kMaxTokens)) || (rc = check_size(fn, "outs", outs, 1, kMaxCols / 2)) ||
+      (rc = check_size(fn, "ins", ins, 1, kMaxCols / 2)) || (rc = check_dtype(fn, "dy", dy_dtype)))
     return rc;
   if (outs * ins > ((int64_t)1 << 31)) return fail(MA_ERR_INVALID_ARG, "%s: outs * ins beyond 2^31", fn);
   if (tokens * outs > kMaxElems || tokens * act_pitch(ins) > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^38 elements", fn);

@@ -127,22 +127,26 @@ __global__ void __launch_bounds__(TL::NT, 2) k_wgrad(const WgradArgs a) {
   const int qw0 = TL::P_BYTES + qr * TL::Q_ROW + ((qc ^ qs) << 4);
   const int qw1 = TL::P_BYTES + qr * TL::Q_ROW + (((qc + TL::QC) ^ qs ^ 2) << 4);
 
+  // a k-tile's rows from a scalar address, the lane's place in them as a 32-bit offset
+  const uint32_t poff = (uint32_t)pr * (uint32_t)(a.outs * elem_bytes<DYD>()) + (uint32_t)(pcol * elem_bytes<DYD>());
+  const uint32_t qoff = (uint32_t)qr * (uint32_t)pitch + (uint32_t)qcol;
+  const uint32_t soff = (uint32_t)qr * (uint32_t)kb + (uint32_t)(qcol / kActBlock);
+  const int64_t prow = (int64_t)a.outs * elem_bytes<DYD>();
+
   Raw8<DYD> p[TL::NP];
   u32x4_t q[TL::NQ];
   uint32_t sc[TL::NQ];
-  auto load = [&](int v) __attribute__((always_inline)) {
+  // A k-tile is whole if its rows are there and, where a row's last chunk of dy
+  // is partial, 8 more rows, into which that chunk is read on.
+  const int64_t slack = a.outs & 7 ? 8 : 0;
+  const int whole_tiles = a.tokens > slack ? (int)((a.tokens - slack) / BK) : 0;
+  auto load_p = [&](int v, auto fast) __attribute__((always_inline)) {
     const int64_t t0 = (int64_t)v * BK;
-    if (t0 + BK + 8 <= a.tokens) {
-      // rows that at least 8 more follow: a chunk past its row's end stays inside dy
+    const unsigned char* base = reinterpret_cast<const unsigned char*>(a.dy) + t0 * prow;
+    if (decltype(fast)::value || v < whole_tiles) {
 #pragma unroll
-      for (int j = 0; j < TL::NP; ++j) p[j] = raw_load<DYD>(elem_ptr<DYD>(a.dy, (t0 + pr + j * TL::P_STEP) * a.outs + pcol));
-#pragma unroll
-      for (int j = 0; j < TL::NQ; ++j) {
-        const int64_t r = t0 + qr + j * TL::Q_STEP;
-        q[j] = *reinterpret_cast<const u32x4_t*>(a.q + r * pitch + qcol);
-        sc[j] = a.qscale[r * kb + qcol / kActBlock];
-      }
-    } else {
+      for (int j = 0; j < TL::NP; ++j) p[j] = raw_load<DYD>(base + j * TL::P_STEP * prow + poff);
+    } else if constexpr (PL == 1) {
 #pragma unroll
       for (int j = 0; j < TL::NP; ++j) {
         const int64_t r = t0 + pr + j * TL::P_STEP;
@@ -150,6 +154,18 @@ __global__ void __launch_bounds__(TL::NT, 2) k_wgrad(const WgradArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < TL::NP; ++j) raw_fix<DYD>(p[j], pcol, a.outs);
+    }
+  };
+  auto load_q = [&](int v, auto fast) __attribute__((always_inline)) {
+    const int64_t t0 = (int64_t)v * BK;
+    const uint8_t *base = a.q + t0 * pitch, *sbase = a.qscale + t0 * kb;
+    if (decltype(fast)::value || t0 + BK <= a.tokens) {
+#pragma unroll
+      for (int j = 0; j < TL::NQ; ++j) {
+        q[j] = *reinterpret_cast<const u32x4_t*>(base + j * TL::Q_STEP * pitch + qoff);
+        sc[j] = (sbase + j * TL::Q_STEP * kb)[soff];
+      }
+    } else {
 #pragma unroll
       for (int j = 0; j < TL::NQ; ++j) {
         const int64_t r = t0 + qr + j * TL::Q_STEP;
@@ -162,15 +178,29 @@ __global__ void __launch_bounds__(TL::NT, 2) k_wgrad(const WgradArgs a) {
       }
     }
   };
-  auto stage = [&](lds_u8_t* st) __attribute__((always_inline)) {
+  auto put_p = [&](lds_u8_t* st, const Raw8<DYD>& x) __attribute__((always_inline)) {
+    u32x4_t w[PL];
+    if constexpr (PL == 1) w[0] = x.u[0];
+    else split_terms(x, w);
 #pragma unroll
-    for (int j = 0; j < TL::NP; ++j) {
-      u32x4_t w[PL];
-      if constexpr (PL == 1) w[0] = p[j].u[0];
-      else split_terms(p[j], w);
+    for (int i = 0; i < PL; ++i) *(lds_u32x4_t*)(st + i * TL::P_PLANE) = w[i];
+  };
+  auto stage_p = [&](int v, lds_u8_t* st, auto fast) __attribute__((always_inline)) {
+    if (PL == 1 || decltype(fast)::value || v < whole_tiles) {
 #pragma unroll
-      for (int i = 0; i < PL; ++i) *(lds_u32x4_t*)(st + pw + i * TL::P_PLANE + j * TL::P_STEP * TL::P_ROW) = w[i];
+      for (int j = 0; j < TL::NP; ++j) put_p(st + pw + j * TL::P_STEP * TL::P_ROW, p[j]);
+    } else {
+      // the last k-tile of fp32 dy is read here, row by row (there are no registers for more)
+#pragma unroll 1
+      for (int j = 0; j < TL::NP; ++j) {
+        const int64_t r = (int64_t)v * BK + pr + j * TL::P_STEP;
+        Raw8<DYD> x = r < a.tokens ? raw_load_row<DYD>(elem_ptr<DYD>(a.dy, r * a.outs), pcol, a.outs) : raw_zero<DYD>();
+        raw_fix<DYD>(x, pcol, a.outs);
+        put_p(st + pw + j * TL::P_STEP * TL::P_ROW, x);
+      }
     }
+  };
+  auto stage_q = [&](lds_u8_t* st) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < TL::NQ; ++j) {
       const float s = act_scale(sc[j]);
@@ -237,32 +267,67 @@ __global__ void __launch_bounds__(TL::NT, 2) k_wgrad(const WgradArgs a) {
     asm volatile("" ::: "memory");
   };
 
+  typedef std::integral_constant<bool, true> Fast;
+  typedef std::integral_constant<bool, false> Any;
   if (v0 < v1) {
-    load(v0);
-    stage(lds);
-    if (v0 + 1 < v1) load(v0 + 1);
+    load_p(v0, Any());
+    load_q(v0, Any());
+    stage_p(v0, lds, Any());
+    stage_q(lds);
+    if (v0 + 1 < v1) {
+      load_p(v0 + 1, Any());
+      load_q(v0 + 1, Any());
+    }
     barrier();
     read(lds, 0);
   }
-  for (int v = v0; v < v1; ++v) {
+  // k-tile v: the staging of v + 1 and the loads of v + 2 go between its MFMAs.
+  // FAST: both exist and are whole, so that all of it is one block of
+  // instructions without branches, interleaved as the groups say.
+  auto tile = [&](int v, auto fast) __attribute__((always_inline)) {
+    constexpr bool F = decltype(fast)::value;
     lds_u8_t* const cur = lds + ((v - v0) & 1) * TL::STAGE;
     lds_u8_t* const nxt = lds + ((v - v0 + 1) & 1) * TL::STAGE;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       if (ks + 1 < KS) {
         read(cur, ks + 1);
-      } else if (v + 1 < v1) {
+      } else if (F || v + 1 < v1) {
         barrier();
         read(nxt, 0);
       }
-      if (ks == KS - 2 && v + 1 < v1) {
-        stage(nxt);
-        if (v + 2 < v1) load(v + 2);
+      // (not FAST: after the MFMAs, whose fragments then leave their registers)
+      if constexpr (!F) {
+        multiply(ks);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      multiply(ks);
+      if (ks == KS / 2 - 1) {
+        if (F || v + 1 < v1) stage_p(v + 1, nxt, fast);
+        if (F || v + 2 < v1) load_p(v + 2, fast);
+      }
+      if (ks == KS - 2) {
+        if (F || v + 1 < v1) stage_q(nxt);
+        if (F || v + 2 < v1) load_q(v + 2, fast);
+      }
+      if constexpr (F) {
+        multiply(ks);
+        // per MFMA up to 3 LDS reads, 3 conversions, a write and a load
+#pragma unroll
+        for (int i = 0; i < TL::FM * TL::FN; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+          __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-  }
+  };
+  const int fast_end = (v1 < whole_tiles ? v1 : whole_tiles) - 2;
+  int v = v0;
+  for (; v < fast_end; ++v) tile(v, Fast());
+  for (; v < v1; ++v) tile(v, Any());
 
   // 32 rows of the wave's block at a time through its own part of LDS, so that
   // stores are 8 consecutive values per lane and whole rows per 8 lanes

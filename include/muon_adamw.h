@@ -411,7 +411,7 @@ int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
  * dy: tokens x outs; q, scale: the checkpoint of x (tokens x ins) as written by
  * ma_act_pack; grad: outs x ins. The held values are used as they are (no
  * second rounding) and dy at its full precision; products are summed in fp32.
- * Limits: tokens <= 2^25, outs, ins <= 2^24, outs * ins <= 2^31. workspace: at
+ * Limits: tokens <= 2^25, outs, ins <= 2^23, outs * ins <= 2^31. workspace: at
  * least ma_act_weight_grad_workspace_size bytes, which may be 0. */
 size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype);
 int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const uint8_t* scale, int64_t tokens,
