@@ -255,7 +255,7 @@ static int wgrad_sizes(const char* fn, int64_t tokens, int64_t outs, int64_t ins
 
 static size_t wgrad_workspace(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype) {
   const int splits = wgrad_splits(tokens, outs, ins, dy_dtype);
-  return splits > 1 ? (size_t)round_up((int64_t)splits * outs * ins * 4, MA_WORKSPACE_ALIGN) : 0;
+  return splits > 1 ? (size_t)(splits * wgrad_partial(outs, ins) * 4) : 0;
 }
 
 size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype) {

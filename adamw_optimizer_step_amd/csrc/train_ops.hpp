@@ -84,10 +84,12 @@ struct WgradArgs {
   const void* dy;             // tokens x outs
   const uint8_t *q, *qscale;  // tokens x ins
   void* grad;                 // outs x ins
-  float* partial;             // [splits][outs][ins], splits > 1
+  float* partial;             // [splits][wgrad_partial], splits > 1
   int64_t tokens;
   int32_t outs, ins, accumulate, splits;
 };
+// elements of one split's partial products (whole cache lines)
+__host__ __device__ constexpr int64_t wgrad_partial(int64_t outs, int64_t ins) { return round_up(outs * ins, 64); }
 int wgrad_splits(int64_t tokens, int64_t outs, int64_t ins, int dy_dt);
 hipError_t launch_wgrad(const WgradArgs& a, int dy_dt, int grad_dt, hipStream_t s);
 

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(TL::NT, 2) k_wgrad(const WgradArgs a) {
       const int n = n0 + wm * TL::WTM + i * 32 + row, k = k0 + wn * TL::WTN + c;
       if (n >= a.outs || k >= a.ins) continue;
       if (!whole) {
-        store_row<DT_F32>(elem_ptr<DT_F32>(a.partial, ((int64_t)split * a.outs + n) * a.ins), k, a.ins, v);
+        store_row<DT_F32>(elem_ptr<DT_F32>(a.partial, split * wgrad_partial(a.outs, a.ins) + (int64_t)n * a.ins), k, a.ins, v);
         continue;
       }
       unsigned char* out = elem_ptr<GD>(a.grad, (int64_t)n * a.ins);
@@ -375,19 +375,14 @@ template <int GD>
 __global__ void __launch_bounds__(256) k_wgrad_join(const WgradArgs a) {
   const int64_t total = (int64_t)a.outs * a.ins, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= total) return;
-  typedef typename U16<DT_F32>::T V;
   float v[4] = {};
   const int n = total - i < 4 ? (int)(total - i) : 4;
-  if (n == 4) {
+  const int64_t stride = wgrad_partial(a.outs, a.ins);   // past the end there is room, not read further
 #pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) {
-      const u32x4_t u = *reinterpret_cast<const V*>(a.partial + s * total + i);
+  for (int s = 0; s < a.splits; ++s) {
+    const u32x4_t u = *reinterpret_cast<const u32x4_t*>(a.partial + s * stride + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += __uint_as_float(u[e]);
-    }
-  } else {
-    for (int s = 0; s < a.splits; ++s)
-      for (int e = 0; e < 3; ++e) v[e] += e < n ? a.partial[s * total + i + e] : 0.0f;
+    for (int e = 0; e < 4; ++e) v[e] += __uint_as_float(u[e]);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -399,21 +394,27 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const WgradArgs a) {
 
 struct WgradPlan { bool big; int splits; };
 
-// Tile and number of splits by the time they should take (us): rounds of
-// blocks over the CUs, each as long as its k-tiles and a fixed part, and the
-// join's traffic.
+// Tile and number of splits by the time they should take (us), from what single
+// launches of 64 .. 4096 tokens took: a fixed part, the k-tiles of the blocks
+// that share a CU (one or two small tiles, one big one, slower as more CUs draw
+// on memory and power), the outputs or partial products written, and the join.
+//   k-tile of 64 tokens, bf16 dy: 128 x 128 0.66 alone, 1.08 for a pair; 256 x 256 1.2 (64 blocks) to 1.6 (256)
+//   k-tile of 32 tokens, fp32 dy: 0.92, 1.5; 1.75 to 2.3
 static WgradPlan wgrad_plan(int64_t tokens, int64_t outs, int64_t ins, int dy_dt) {
-  const int64_t bk = dy_dt == DT_F32 ? 32 : 64, vt = (tokens + bk - 1) / bk;
+  const bool f32 = dy_dt == DT_F32;
+  const int64_t bk = f32 ? 32 : 64, vt = (tokens + bk - 1) / bk;
+  const double mb = (double)outs * (double)ins * 4e-6;   // of one fp32 result
   WgradPlan best{false, 1};
   double best_us = 1e30;
   for (int big = 0; big < 2; ++big) {
-    const int64_t tm = (outs + (big ? 255 : 127)) / (big ? 256 : 128), tn = (ins + (big ? 255 : 127)) / (big ? 256 : 128);
-    const int64_t slots = big ? 256 : 512;
-    const double tile_us = (big ? 1.8 : 1.3) * (dy_dt == DT_F32 ? 1.5 : 1.0), fixed_us = 5.0;
+    const int64_t edge = big ? 256 : 128, tiles = ((outs + edge - 1) / edge) * ((ins + edge - 1) / edge);
     for (int64_t s = 1; s <= 64 && s <= (vt > 1 ? vt : 1); ++s) {
-      const int64_t jobs = tm * tn * s, rounds = (jobs + slots - 1) / slots;
-      double us = (double)rounds * ((double)((vt + s - 1) / s) * tile_us + fixed_us);
-      if (s > 1) us += 4.0 + (double)(s + 1) * (double)outs * (double)ins * 4.0 / 4e6;
+      const int64_t jobs = tiles * s, rounds = (jobs + 255) / 256;   // blocks per CU
+      const double full = jobs < 256 ? (double)jobs / 256 : 1.0;
+      const double small_us = (double)(rounds / 2) * (f32 ? 1.5 : 1.08) + (double)(rounds % 2) * (f32 ? 0.92 : 0.66);
+      const double big_us = (double)rounds * (f32 ? 1.75 + 0.55 * full : 1.2 + 0.4 * full);
+      double us = 5.5 + (double)((vt + s - 1) / s) * (big ? big_us : small_us) + (double)s * mb / 5.5;
+      if (s > 1) us += 2.5 + (double)(s + 1) * mb / 6.5;
       if (us < best_us * 0.999) { best_us = us; best = {big != 0, (int)s}; }
     }
   }
