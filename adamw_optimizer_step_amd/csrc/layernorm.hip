@@ -25,7 +25,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[16]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = wave_sum_dpp(v[n]);
   if constexpr (G > 64) {
-    const int wave = threadIdx.x >> 6;
+    const int wave = threadIdx.x % G >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int n = 0; n < N; ++n) part[n][wave] = v[n];
@@ -122,16 +122,19 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
   }
 }
 
-// The backward pass: a fixed number of blocks, each with a contiguous share of
-// the rows, keeps the sums for dgain and dbias of its columns in registers and
-// writes them once; k_norm_cols adds the blocks' sums in order.
+// The backward pass: as many blocks as are resident at once, each with a
+// contiguous share of the rows, its groups taking a row each at a time, keep the
+// sums for dgain and dbias of their columns in registers; the groups' sums are
+// added in LDS, pairs of halves, and written once per block. k_norm_cols adds the
+// blocks' sums in order.
+constexpr int norm_bwd_threads(int G) { return G < 512 ? 512 : G; }
 template <int XD> constexpr int raw_dt() { return XD == DT_ACT8 ? DT_BF16 : XD; }
 
 template <int XD, int DYD, int DXD, int G, int CH>
-__global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs a) {
-  constexpr int ROWS = norm_threads(G) / G;
-  __shared__ float part[2][2][16];
-  __shared__ float join[G == 64 ? 512 * CH : 1];
+__global__ void __launch_bounds__(norm_bwd_threads(G)) k_norm_bwd(const NormBwdArgs a) {
+  constexpr int ROWS = norm_bwd_threads(G) / G;
+  __shared__ float part[2][ROWS][2][16];
+  __shared__ float join[ROWS > 1 ? ROWS / 2 : 1][ROWS > 1 ? G * CH * 8 : 1];
   const int t = threadIdx.x % G, group = threadIdx.x / G;
   const float per = 1.0f / (float)a.cols;
   const int64_t pitch = act_pitch(a.cols);
@@ -179,7 +182,8 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
   int flip = 0;
   for (int64_t u = u0; u < u1; ++u, flip ^= 1) {
     const int64_t row = u * ROWS + group;
-    if (G == 64 && row >= a.rows) break;
+    const bool valid = row < a.rows;
+    if (G == 64 && !valid) break;   // (wider groups meet at barriers)
     const Row now = AHEAD ? next : load(row);
     if constexpr (AHEAD) next = load(u + 1 < u1 ? row + ROWS : a.rows);
     float s[2] = {0.0f, 0.0f};
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float(&x)[8] = xh[HOLD ? c : 0], (&d)[8] = g[HOLD ? c : 0], w[8];
-      if ((c * G + t) * 8 >= a.cols) continue;
+      if (!valid || (c * G + t) * 8 >= a.cols) continue;
       chunk(now, c, x, d, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -224,14 +228,14 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
         s[1] = __builtin_fmaf(d[e], x[e], s[1]);
       }
     }
-    group_sum<G>(s, part[flip]);
+    group_sum<G>(s, part[flip][group]);
     const float m0 = s[0] * per, m1 = s[1] * per;
     const Row again = HOLD ? Row() : load(row);
     unsigned char* dst = elem_ptr<DXD>(a.dx, row * a.cols);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * G + t) * 8;
-      if (col >= a.cols) continue;
+      if (!valid || col >= a.cols) continue;
       float(&x)[8] = xh[HOLD ? c : 0], (&d)[8] = g[HOLD ? c : 0], w[8], out[8];
       if constexpr (!HOLD) {
         chunk(again, c, x, d, w);
@@ -249,22 +253,24 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_bwd(const NormBwdArgs 
     // by 32 columns, so that k_norm_cols reads one contiguous stretch
     float* const out = a.partial + (int64_t)which * round_up(a.cols, 32) * a.blocks;
     float(&v)[CH][8] = which ? db : dg;
-    if constexpr (G == 64) {
-      // the block's rows in order of their wave
-      for (int w = 0; w < ROWS; ++w) {
-        __syncthreads();
-        if (group != w) continue;
+#pragma unroll
+    for (int half = ROWS / 2; half > 0; half /= 2) {
+      __syncthreads();
+      if (group >= half && group < 2 * half) {
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* p = &join[(c * 8 + e) * 64 + t];
-            v[c][e] = w ? *p + v[c][e] : v[c][e];
-            if (w + 1 < ROWS) *p = v[c][e];
-          }
+          for (int e = 0; e < 8; ++e) join[group - half][(c * 8 + e) * G + t] = v[c][e];
       }
-      if (group != ROWS - 1) continue;
+      __syncthreads();
+      if (group < half) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[c][e] += join[group][(c * 8 + e) * G + t];
+      }
     }
+    if (group) continue;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * G + t) * 8;
@@ -340,15 +346,24 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dt, int y_dt, hipStream_t
   return y_dt == DT_F32 ? norm_fwd<DT_BF16, DT_F32>(a, s) : norm_fwd<DT_BF16, DT_BF16>(a, s);
 }
 
-// as many as are resident at once: 16 waves per CU
+// As many as are resident at once (16 waves per CU); where a row takes 256 lanes
+// or more at least 4 steps each, down to 128 blocks: every block writes, and
+// k_norm_cols reads, two rows of sums (1537 x 2047, fp32 dy: 11 + 4.3 us with 193
+// blocks, 12.4 + 3.9 with 385; 500 x 4096: 11.6 + 3.8 with 128, 13.2 + 5 with 500).
 int norm_bwd_blocks(int64_t rows, int64_t cols) {
   int64_t units = rows, most = 0;
+  bool wide = false;
   (void)norm_bwd_shape(cols, [&](auto sh) {
-    constexpr int G = decltype(sh)::G;
-    units = (rows + norm_threads(G) / G - 1) / (norm_threads(G) / G);
-    most = 256 * 16 * 64 / norm_threads(G);
+    constexpr int G = decltype(sh)::G, T = norm_bwd_threads(G);
+    units = (rows + T / G - 1) / (T / G);
+    most = 256 * 16 * 64 / T;
+    wide = G >= 256;
     return hipSuccess;
   });
+  if (wide) {
+    const int64_t want = (units + 3) / 4, least = units < 128 ? units : 128;
+    units = want > least ? want : least;
+  }
   return (int)(units < most ? units : most);
 }
 
@@ -356,7 +371,7 @@ template <int XD, int DYD, int DXD>
 static hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
   return norm_bwd_shape(a.cols, [&](auto sh) {
     constexpr int G = decltype(sh)::G, CH = decltype(sh)::CH;
-    hipLaunchKernelGGL((k_norm_bwd<XD, DYD, DXD, G, CH>), dim3((unsigned)a.blocks), dim3(norm_threads(G)), 0, s, a);
+    hipLaunchKernelGGL((k_norm_bwd<XD, DYD, DXD, G, CH>), dim3((unsigned)a.blocks), dim3(norm_bwd_threads(G)), 0, s, a);
     return hipGetLastError();
   });
 }
