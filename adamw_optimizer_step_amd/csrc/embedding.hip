@@ -277,6 +277,22 @@ __device__ __forceinline__ void embed_sum(const EmbedBwdArgs& a, int32_t pos, in
   }
 }
 
+// A row's sum, scaled, to the gradient, or added to what is there.
+template <int CH, bool ACC>
+__device__ __forceinline__ void embed_store(const EmbedBwdArgs& a, int64_t v, int col, float (&acc)[CH][8]) {
+  unsigned char* out = reinterpret_cast<unsigned char*>(a.grad + v * a.cols);
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int cc = col + k * 512;
+    if (cc >= a.cols) continue;
+    float old[8] = {};
+    if constexpr (ACC) raw_f32_row<DT_F32>(raw_load_row<DT_F32>(out, cc, a.cols), cc, a.cols, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[k][e] = ACC ? __fadd_rn(old[e], __fmul_rn(acc[k][e], a.scale)) : acc[k][e] * a.scale;
+    store_row<DT_F32>(out, cc, a.cols, acc[k]);
+  }
+}
+
 template <int DD, int CH, bool ACC>
 __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int piece_blocks) {
   const int lane = threadIdx.x & 63;
@@ -321,17 +337,7 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int pie
     const int64_t s = __builtin_amdgcn_readlane(starts, r);
     const int32_t pos = lane < c ? a.order[s + lane] : 0;
     embed_sum<DD, CH>(a, pos, 0, c, col, acc);
-    unsigned char* out = reinterpret_cast<unsigned char*>(a.grad + v * a.cols);
-#pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int cc = col + k * 512;
-      if (cc >= a.cols) continue;
-      float old[8] = {};
-      if constexpr (ACC) raw_f32_row<DT_F32>(raw_load_row<DT_F32>(out, cc, a.cols), cc, a.cols, old);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[k][e] = ACC ? __fadd_rn(old[e], __fmul_rn(acc[k][e], a.scale)) : acc[k][e] * a.scale;
-      store_row<DT_F32>(out, cc, a.cols, acc[k]);
-    }
+    embed_store<CH, ACC>(a, v, col, acc);
   }
 }
 
@@ -394,6 +400,76 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdAr
   }
 }
 
+// ---------------------------------------------------------------------------
+// backward of few tokens (at most kEmbedDirect), in one launch and without a
+// sort. The first blocks take a token per wave: the wave has all tokens in
+// registers, and if its token is the first of its row it finds the others by
+// comparison and sums them in ascending position. When the gradient is written
+// whole, the other blocks write zeros to the rows that no token names,
+// kDirectRows each, flagged in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kDirectRows = 64, kDirectWords = kEmbedDirect / 64;
+
+template <int DD, int CH, bool ACC, bool WIDE>
+__global__ void __launch_bounds__(256) k_embed_direct(const EmbedBwdArgs a, int token_blocks) {
+  __shared__ int32_t found[4][kEmbedDirect];
+  __shared__ uint32_t named[kDirectRows];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = blockIdx.y * 512 * CH + lane * 8;
+  const int n = (int)a.n_tokens;
+  if ((int)blockIdx.x < token_blocks) {
+    uint32_t t[kDirectWords];
+    tokens32<WIDE, kDirectWords>(a.tokens, 0, n, lane, t);
+    const int item = (int)blockIdx.x * 4 + wave;
+    if (item >= n) return;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int w = 0; w < kDirectWords; ++w)
+      if (item / 64 == w) mine = t[w];
+    const uint32_t v = __builtin_amdgcn_readlane(mine, item % 64);
+    if (v >= (uint32_t)a.rows) return;
+    int count = 0;
+#pragma unroll
+    for (int w = 0; w < kDirectWords; ++w) {
+      const uint64_t m = __ballot(t[w] == v);
+      if (!m) continue;
+      if (!count && w * 64 + __builtin_ctzll(m) != item) return;   // an earlier token's wave has the row
+      if (t[w] == v) found[wave][count + __builtin_popcountll(m & (((uint64_t)1 << lane) - 1))] = w * 64 + lane;
+      count += __builtin_popcountll(m);
+    }
+    float acc[CH][8], more[CH][8];
+    for (int k = 0; k < count; k += 64) {
+      const int c = count - k < 64 ? count - k : 64;
+      embed_sum<DD, CH>(a, lane < c ? found[wave][k + lane] : 0, 0, c, col, k ? more : acc);
+      if (k) {
+#pragma unroll
+        for (int x = 0; x < CH; ++x)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[x][e] += more[x][e];
+      }
+    }
+    embed_store<CH, ACC>(a, v, col, acc);
+    return;
+  }
+  const int64_t first = (int64_t)((int)blockIdx.x - token_blocks) * kDirectRows;
+  if (threadIdx.x < kDirectRows) named[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEmbedDirect; i += 256) {
+    if (i + (int)threadIdx.x < n) {
+      const int64_t v = token_at(a.tokens, WIDE, i + threadIdx.x) - first;
+      if (v >= 0 && v < kDirectRows) named[v] = 1;   // (every writer writes the same)
+    }
+  }
+  __syncthreads();
+  for (int r = wave; r < kDirectRows && first + r < a.rows; r += 4) {
+    if (named[r]) continue;
+    float* out = a.grad + (first + r) * a.cols;
+    for (int c = blockIdx.y * 512 * CH + lane; c < a.cols && c < (blockIdx.y + 1) * 512 * CH; c += 64) out[c] = 0.0f;
+  }
+}
+
 // blocks of the sort: one per CU; more where a block would own more rows than its counters hold
 static int embed_log2nb(int64_t rows) {
   int log2nb = 8;
@@ -404,7 +480,8 @@ static int64_t embed_per_block(int64_t rows) { return (rows + ((int64_t)1 << emb
 static int64_t embed_pieces(int64_t n_tokens) { return (n_tokens + kEmbedPiece - 1) / kEmbedPiece; }
 
 size_t embed_bwd_workspace(int64_t rows, int64_t cols, int64_t n_tokens) {
-  const int64_t partial = n_tokens > kEmbedPiece ? 2 * embed_pieces(n_tokens) * cols * 4 : 0;
+  if (n_tokens <= kEmbedDirect) return 256;   // (not used; 0 would be an error)
+  const int64_t partial = 2 * embed_pieces(n_tokens) * cols * 4;
   const int64_t slots = embed_per_block(rows) << embed_log2nb(rows);
   return (size_t)(256 + 2 * round_up(slots * 4, 256) + 2 * round_up(n_tokens * 4, 256) + round_up(partial, 256));
 }
@@ -424,7 +501,16 @@ void embed_bwd_carve(EmbedBwdArgs& a, unsigned char* ws) {
 
 template <int DD, int CH>
 static void embed_sum_launch(const EmbedBwdArgs& a, hipStream_t s) {
-  const int64_t pieces = a.n_tokens > kEmbedPiece ? embed_pieces(a.n_tokens) : 0;
+  if (a.n_tokens <= kEmbedDirect) {
+    const int tb = (int)((a.n_tokens + 3) / 4);
+    const int64_t fill = a.accumulate ? 0 : (a.rows + kDirectRows - 1) / kDirectRows;
+    const dim3 grid((unsigned)(tb + fill), (unsigned)((a.cols + 512 * CH - 1) / (512 * CH)));
+    auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a, tb); };
+    if (a.accumulate) a.wide ? go(k_embed_direct<DD, CH, true, true>) : go(k_embed_direct<DD, CH, true, false>);
+    else a.wide ? go(k_embed_direct<DD, CH, false, true>) : go(k_embed_direct<DD, CH, false, false>);
+    return;
+  }
+  const int64_t pieces = embed_pieces(a.n_tokens);
   const int pb = (int)((pieces + 3) / 4);
   const int64_t items = (int64_t)((a.per_block + kEmbedGroup - 1) / kEmbedGroup) << a.log2nb;
   const dim3 grid((unsigned)(pb + (items + 3) / 4), (unsigned)((a.cols + 512 * CH - 1) / (512 * CH)));
@@ -434,10 +520,13 @@ static void embed_sum_launch(const EmbedBwdArgs& a, hipStream_t s) {
 
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dout_dt, hipStream_t s) {
   if (a.n_tokens == 0 && a.accumulate) return hipSuccess;
-  if (a.wide) hipLaunchKernelGGL((k_embed_bin<true>), dim3(1u << a.log2nb), dim3(kBinThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_embed_bin<false>), dim3(1u << a.log2nb), dim3(kBinThreads), 0, s, a);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  const bool direct = a.n_tokens <= kEmbedDirect;
+  hipError_t err = hipSuccess;
+  if (!direct) {
+    if (a.wide) hipLaunchKernelGGL((k_embed_bin<true>), dim3(1u << a.log2nb), dim3(kBinThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_embed_bin<false>), dim3(1u << a.log2nb), dim3(kBinThreads), 0, s, a);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+  }
   if (dout_dt == DT_F32) {
     if (a.cols <= 512) embed_sum_launch<DT_F32, 1>(a, s);
     else embed_sum_launch<DT_F32, 2>(a, s);
@@ -446,7 +535,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dout_dt, hipStream_t s) {
     else embed_sum_launch<DT_BF16, 2>(a, s);
   }
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  if (a.n_tokens > kEmbedPiece) {
+  if (!direct) {
     hipLaunchKernelGGL(k_embed_join, dim3((unsigned)((embed_pieces(a.n_tokens) + kJoinPieces - 1) / kJoinPieces), (unsigned)((a.cols + 255) / 256)),
                        dim3(kJoinWaves * 64), 0, s, a);
     err = hipGetLastError();

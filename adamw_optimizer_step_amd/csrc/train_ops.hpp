@@ -22,6 +22,8 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hip
 // Runs of the sorted tokens longer than this are summed in pieces of as many
 // sorted positions, one wave each, and joined in order.
 constexpr int kEmbedPiece = 32;
+// Up to this many tokens the rows' waves look for their tokens themselves.
+constexpr int kEmbedDirect = 512;
 struct EmbedBwdArgs {
   const void* dout;
   const void* tokens;

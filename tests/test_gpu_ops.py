@@ -117,6 +117,8 @@ def test_embedding_shapes_and_defaults():
     (257, 512, 200, F32, "zipf", 0), (1000, 333, 3000, F32, "zipf", 1), (97, 1030, 1500, BF16, "zipf", 0),
     (30, 64, 5000, BF16, "one", 0), (700, 2050, 513, F32, "outside", 0), (66000, 16, 4097, BF16, "zipf", 0),
     (200000, 5, 2500, F32, "spread", 0), (40, 24, 100, F32, "none", 0), (3, 16, 20000, F32, "spread", 0),
+    (70, 520, 512, BF16, "one", 0), (70, 520, 513, BF16, "one", 0), (9, 33, 511, F32, "outside", 1), (9, 33, 700, F32, "none", 0),
+    (1 << 18, 3, 600, F32, "zipf", 0), (513, 8, 17000, BF16, "zipf", 0),
 ])
 @pytest.mark.parametrize("acc", [False, True])
 def test_embedding_backward(rows, cols, n, dd, kind, off, acc):
