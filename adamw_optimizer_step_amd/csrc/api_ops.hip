@@ -173,9 +173,13 @@ int ma_layernorm_forward(const void* x, int32_t x_dtype, int64_t rows, int64_t c
   return done(launch_norm_fwd(a, x_dtype, y_dtype, s), fn);
 }
 
+static size_t norm_workspace(int64_t rows, int64_t cols) {
+  return norm_bwd_direct(rows) ? 0 : (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * round_up(cols, 32) * 4, MA_WORKSPACE_ALIGN);
+}
+
 size_t ma_layernorm_workspace_size(int64_t rows, int64_t cols) {
   if (check_matrix("ma_layernorm_workspace_size", rows, 0, kMaxRows, cols, kMaxNormCols)) return 0;
-  return (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * round_up(cols, 32) * 4, MA_WORKSPACE_ALIGN);
+  return norm_workspace(rows, cols);
 }
 
 int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const uint8_t* ckpt_q, const uint8_t* ckpt_scale,
@@ -195,7 +199,7 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
     return fail(MA_ERR_UNSUPPORTED, "%s: dx has the type of x, or of dy where x is a checkpoint", fn);
   const int64_t pitch = act_pitch(cols);
   const bool sums = dgain || dbias;
-  const size_t need = sums ? (size_t)round_up(norm_bwd_blocks(rows, cols) * 2 * round_up(cols, 32) * 4, MA_WORKSPACE_ALIGN) : 0;
+  const size_t need = sums ? norm_workspace(rows, cols) : 0;
   const Buf bufs[] = {{dy, rows * cols * dt_size(dy_dtype), (int)dt_size(dy_dtype), false, false, "dy"},
                       {x, held ? 0 : rows * cols * dt_size(x_dtype), held ? 1 : (int)dt_size(x_dtype), false, false, "x"},
                       {ckpt_q, rows * pitch, 16, false, !held, "x and the checkpoint's q"},
@@ -210,7 +214,7 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
   if (rows == 0 && (!sums || accumulate)) return MA_OK;
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const NormBwdArgs a{dy, x, ckpt_q, ckpt_scale, stats, gain, dx, dgain, dbias, sums ? reinterpret_cast<float*>(workspace) : nullptr,
+  const NormBwdArgs a{dy, x, ckpt_q, ckpt_scale, stats, gain, dx, dgain, dbias, need ? reinterpret_cast<float*>(workspace) : nullptr,
                       rows, (int32_t)cols, accumulate, norm_bwd_blocks(rows, cols)};
   ProfScope ps(MA_K_LAYERNORM, s);
   return done(launch_norm_bwd(a, held ? DT_ACT8 : x_dtype, dy_dtype, dx_dtype, s), fn);

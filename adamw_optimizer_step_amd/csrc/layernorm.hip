@@ -130,11 +130,51 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
 constexpr int norm_bwd_threads(int G) { return G < 512 ? 512 : G; }
 template <int XD> constexpr int raw_dt() { return XD == DT_ACT8 ? DT_BF16 : XD; }
 
-template <int XD, int DYD, int DXD, int G, int CH>
+// The sums for dgain and dbias of 64 columns over all of few rows (at most
+// kNormDirectRows), by the blocks of the same launch that take no rows: a lane per
+// column, the block's waves every W-th row, then the waves in order. Reads x and
+// dy once more, from the caches, and saves the partial sums and a launch.
+template <int XD, int DYD, int W>
+__device__ __forceinline__ void norm_cols_direct(const NormBwdArgs& a, int tile, float (*part)[2][64]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = tile * 64 + lane;
+  const int64_t pitch = act_pitch(a.cols);
+  float dg = 0.0f, db = 0.0f;
+  if (col < a.cols) {
+#pragma unroll 16
+    for (int row = wave; row < (int)a.rows; row += W) {
+      float x;
+      if constexpr (XD == DT_ACT8)
+        x = __builtin_amdgcn_cvt_f32_fp8(a.q[row * pitch + col], 0) * act_scale(a.qscale[row * (pitch / kActBlock) + col / kActBlock]);
+      else
+        x = load1<raw_dt<XD>()>(a.x, (int64_t)row * a.cols + col);
+      const float d = load1<DYD>(a.dy, (int64_t)row * a.cols + col);
+      dg = __builtin_fmaf(d, (x - a.stats[2 * row]) * a.stats[2 * row + 1], dg);
+      db += d;
+    }
+  }
+  part[wave][0][lane] = dg;
+  part[wave][1][lane] = db;
+  __syncthreads();
+  float* out = wave == 0 ? a.dgain : (wave == 1 ? a.dbias : nullptr);
+  if (!out || col >= a.cols) return;
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) t += part[w][wave][lane];
+  out[col] = a.accumulate ? __fadd_rn(out[col], t) : t;
+}
+
+template <int XD, int DYD, int DXD, int G, int CH, bool DIRECT>
 __global__ void __launch_bounds__(norm_bwd_threads(G)) k_norm_bwd(const NormBwdArgs a) {
-  constexpr int ROWS = norm_bwd_threads(G) / G;
+  constexpr int ROWS = norm_bwd_threads(G) / G, W = norm_bwd_threads(G) / 64;
   __shared__ float part[2][ROWS][2][16];
   __shared__ float join[ROWS > 1 ? ROWS / 2 : 1][ROWS > 1 ? G * CH * 8 : 1];
+  if constexpr (DIRECT) {
+    __shared__ float cols[W][2][64];
+    if ((int)blockIdx.x >= a.blocks) {
+      norm_cols_direct<XD, DYD, W>(a, (int)blockIdx.x - a.blocks, cols);
+      return;
+    }
+  }
   const int t = threadIdx.x % G, group = threadIdx.x / G;
   const float per = 1.0f / (float)a.cols;
   const int64_t pitch = act_pitch(a.cols);
@@ -247,7 +287,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(G)) k_norm_bwd(const NormBwdA
       store_row<DXD>(dst, col, a.cols, out);
     }
   }
-  if (!a.partial) return;
+  if (DIRECT || !a.partial) return;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     // by 32 columns, so that k_norm_cols reads one contiguous stretch
@@ -320,7 +360,7 @@ static hipError_t norm_fwd_shape(int64_t cols, F&& f) {
 template <typename F>
 static hipError_t norm_bwd_shape(int64_t cols, F&& f) {
   if (cols <= 512) return f(NormShape<64, 1>());
-  if (cols <= 1024) return f(NormShape<64, 2>());
+  if (cols <= 1024) return f(NormShape<128, 1>());
   if (cols <= 2048) return f(NormShape<256, 1>());
   if (cols <= 4096) return f(NormShape<512, 1>());
   if (cols <= 8192) return f(NormShape<1024, 1>());
@@ -346,6 +386,10 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dt, int y_dt, hipStream_t
   return y_dt == DT_F32 ? norm_fwd<DT_BF16, DT_F32>(a, s) : norm_fwd<DT_BF16, DT_BF16>(a, s);
 }
 
+// Whether the rows are so few that no partial sums are kept.
+constexpr int64_t kNormDirectRows = 512;
+bool norm_bwd_direct(int64_t rows) { return rows <= kNormDirectRows; }
+
 // As many as are resident at once (16 waves per CU); where a row takes 256 lanes
 // or more at least 4 steps each, down to 128 blocks: every block writes, and
 // k_norm_cols reads, two rows of sums (1537 x 2047, fp32 dy: 11 + 4.3 us with 193
@@ -360,7 +404,7 @@ int norm_bwd_blocks(int64_t rows, int64_t cols) {
     wide = G >= 256;
     return hipSuccess;
   });
-  if (wide) {
+  if (wide && !norm_bwd_direct(rows)) {
     const int64_t want = (units + 3) / 4, least = units < 128 ? units : 128;
     units = want > least ? want : least;
   }
@@ -371,7 +415,11 @@ template <int XD, int DYD, int DXD>
 static hipError_t norm_bwd(const NormBwdArgs& a, hipStream_t s) {
   return norm_bwd_shape(a.cols, [&](auto sh) {
     constexpr int G = decltype(sh)::G, CH = decltype(sh)::CH;
-    hipLaunchKernelGGL((k_norm_bwd<XD, DYD, DXD, G, CH>), dim3((unsigned)a.blocks), dim3(norm_bwd_threads(G)), 0, s, a);
+    const int tiles = a.dgain || a.dbias ? (a.cols + 63) / 64 : 0;
+    if (norm_bwd_direct(a.rows))
+      hipLaunchKernelGGL((k_norm_bwd<XD, DYD, DXD, G, CH, true>), dim3((unsigned)(a.blocks + tiles)), dim3(norm_bwd_threads(G)), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_norm_bwd<XD, DYD, DXD, G, CH, false>), dim3((unsigned)a.blocks), dim3(norm_bwd_threads(G)), 0, s, a);
     return hipGetLastError();
   });
 }
@@ -384,7 +432,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dt, int dy_dt, int dx_dt,
     else if (x_dt == DT_F32) err = dy_dt == DT_F32 ? norm_bwd<DT_F32, DT_F32, DT_F32>(a, s) : norm_bwd<DT_F32, DT_BF16, DT_F32>(a, s);
     else err = dy_dt == DT_F32 ? norm_bwd<DT_BF16, DT_F32, DT_BF16>(a, s) : norm_bwd<DT_BF16, DT_BF16, DT_BF16>(a, s);
   }
-  if (err != hipSuccess || (!a.dgain && !a.dbias)) return err;
+  if (err != hipSuccess || (!a.dgain && !a.dbias) || (a.rows > 0 && norm_bwd_direct(a.rows))) return err;
   hipLaunchKernelGGL(k_norm_cols, dim3((unsigned)((a.cols + 31) / 32), 2), dim3(1024), 0, s, a);
   return hipGetLastError();
 }

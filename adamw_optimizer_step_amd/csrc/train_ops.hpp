@@ -63,11 +63,12 @@ struct NormBwdArgs {
   const float *stats, *gain;
   void* dx;
   float *dgain, *dbias;       // either may be null
-  float* partial;             // [2][cols / 32][blocks][32]
+  float* partial;             // [2][cols / 32][blocks][32]; null if not kept
   int64_t rows;
   int32_t cols, accumulate, blocks;
 };
 int norm_bwd_blocks(int64_t rows, int64_t cols);
+bool norm_bwd_direct(int64_t rows);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dt, int dy_dt, int dx_dt, hipStream_t s);
 
 // ---- 8-bit activation checkpoints ----

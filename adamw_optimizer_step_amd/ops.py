@@ -275,8 +275,9 @@ def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias
 
 
 def layernorm_workspace_size(rows: int, cols: int) -> int:
+    """Bytes of workspace (0: none needed)."""
     n = L.lib().ma_layernorm_workspace_size(rows, cols)
-    if n == 0 and rows != 0:
+    if n == 0 and not (0 <= rows <= 1 << 24 and 1 <= cols <= 16384):
         L.check(L.MA_ERR_INVALID_ARG)
     return int(n)
 
@@ -312,10 +313,11 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
         nonlocal dx
         if dx is None:
             dx = torch.empty(dy.shape, dtype=dx_dtype, device=dev)
-        ws = _workspace(workspace, layernorm_workspace_size(rows, cols), dev) if sums else None
+        need = layernorm_workspace_size(rows, cols) if sums else 0
+        ws = _workspace(workspace, need, dev) if need or workspace is not None else None
         L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, _ptr(q), _ptr(sc), rows, cols, stats.data_ptr(),
                                               _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
-                                              _ptr(ws), ws.numel() if sums else 0, s))
+                                              _ptr(ws), ws.numel() if ws is not None else 0, s))
         return dx
     return _launch(dev, stream, go)
 

@@ -383,7 +383,7 @@ int ma_layernorm_forward(const void* x, int32_t x_dtype, int64_t rows, int64_t c
  *   dgain (+)= sum over rows of dy * xh;  dbias (+)= sum over rows of dy
  * dx has x's type, or dy's where x is a checkpoint. dgain and dbias (cols fp32
  * values) may each be null; with both null no workspace is needed, else at
- * least ma_layernorm_workspace_size bytes (0 also for rows = 0). accumulate
+ * least ma_layernorm_workspace_size bytes, which may be 0 (few rows). accumulate
  * applies to dgain and dbias. */
 size_t ma_layernorm_workspace_size(int64_t rows, int64_t cols);
 int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const uint8_t* ckpt_q,

@@ -68,7 +68,7 @@ BAD = [
     ("ma_layernorm_backward", dict(x=None), INV), ("ma_layernorm_backward", dict(x=None, ckpt_q=at(8)), INV),
     ("ma_layernorm_backward", dict(ckpt_q=at(8), ckpt_scale=at(9)), INV), ("ma_layernorm_backward", dict(stats=None), INV),
     ("ma_layernorm_backward", dict(dx=at(0)), INV), ("ma_layernorm_backward", dict(dgain=at(6)), INV),
-    ("ma_layernorm_backward", dict(workspace=None), WS), ("ma_layernorm_backward", dict(workspace_bytes=8), WS),
+    ("ma_layernorm_backward", dict(rows=1000, workspace=None), WS), ("ma_layernorm_backward", dict(rows=1000, workspace_bytes=8), WS),
     ("ma_layernorm_backward", dict(accumulate=-1), INV),
     ("ma_layernorm_backward", dict(x=None, ckpt_q=at(8), ckpt_scale=at(9), dy_dtype=0, dx_dtype=1), UNS),
     ("ma_act_pack", dict(x=None), INV), ("ma_act_pack", dict(q=at(1) + 4), INV), ("ma_act_pack", dict(q=at(0)), INV),
@@ -104,7 +104,7 @@ def test_empty_calls_are_no_ops():
 def test_workspace_sizes():
     assert ma.embedding_workspace_size(100, 64, 0) >= 256
     assert ma.embedding_workspace_size(50304, 1024, 49152) >= 2 * 4 * (50304 + 49152)
-    assert ma.layernorm_workspace_size(0, 64) == 0 and ma.layernorm_workspace_size(1, 64) >= 2 * 64 * 4
+    assert ma.layernorm_workspace_size(0, 64) == 0 and ma.layernorm_workspace_size(1, 64) == 0 and ma.layernorm_workspace_size(5000, 64) >= 2 * 64 * 4
     assert ma.act_weight_grad_workspace_size(0, 4, 4) == 0
     for f, a in ((ma.embedding_workspace_size, (0, 1, 1)), (ma.layernorm_workspace_size, (5, 1 << 20)),
                  (ma.act_weight_grad_workspace_size, (5, 0, 3))):
