@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(256) k_act_pack(const ActArgs a) {
     raw[u] = raw_zero<XD>();
     col[u] = 0;
     if (b < total) {
-      const uint32_t row = (uint32_t)b / (uint32_t)kb;   // rows * pitch <= 2^38: at most 2^31 blocks
+      const uint32_t row = (uint32_t)b / (uint32_t)kb;   // rows * pitch <= 2^36: at most 2^29 blocks
       const int at = (int)((uint32_t)b - row * (uint32_t)kb) * kActBlock + lane16 * 8;
       if (at < a.cols) {
         raw[u] = raw_load_row<XD, NT>(elem_ptr<XD>(a.x, (int64_t)row * a.cols), at, a.cols);

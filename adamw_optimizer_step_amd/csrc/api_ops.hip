@@ -14,7 +14,8 @@ namespace {
 
 // size limits: keep every launch within 2^32 threads and every index within its type
 constexpr int64_t kMaxRows = (int64_t)1 << 24, kMaxCols = (int64_t)1 << 24, kMaxTokens = (int64_t)1 << 25;
-constexpr int64_t kMaxElems = (int64_t)1 << 38;
+constexpr int64_t kMaxEmbedCols = (int64_t)1 << 20;
+constexpr int64_t kMaxElems = (int64_t)1 << 36;
 
 bool dt_ok(int dt) { return dt == MA_F32 || dt == MA_BF16; }
 int64_t dt_size(int dt) { return dt == MA_BF16 ? 2 : 4; }
@@ -56,7 +57,7 @@ int check_size(const char* fn, const char* what, int64_t v, int64_t lo, int64_t 
 int check_matrix(const char* fn, int64_t rows, int64_t row_lo, int64_t row_hi, int64_t cols, int64_t col_hi) {
   int rc;
   if ((rc = check_size(fn, "rows", rows, row_lo, row_hi)) || (rc = check_size(fn, "cols", cols, 1, col_hi))) return rc;
-  if (rows * cols > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^38 elements", fn);
+  if (rows * cols > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
   return MA_OK;
 }
 
@@ -82,8 +83,8 @@ int done(hipError_t err, const char* fn) { return err == hipSuccess ? MA_OK : hi
 
 int embedding_sizes(const char* fn, int64_t rows, int64_t cols, int64_t n_tokens) {
   int rc;
-  if ((rc = check_matrix(fn, rows, 1, kMaxRows, cols, kMaxCols)) || (rc = check_size(fn, "n_tokens", n_tokens, 0, kMaxTokens))) return rc;
-  if (n_tokens * cols > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^38 elements", fn);
+  if ((rc = check_matrix(fn, rows, 1, kMaxRows, cols, kMaxEmbedCols)) || (rc = check_size(fn, "n_tokens", n_tokens, 0, kMaxTokens))) return rc;
+  if (n_tokens * cols > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
   return MA_OK;
 }
 
@@ -226,7 +227,7 @@ static int act_call(const char* fn, const void* x, int32_t dtype, bool pack, int
   int rc;
   if ((rc = check_matrix(fn, rows, 0, kMaxRows, cols, kMaxCols)) || (rc = check_dtype(fn, pack ? "x" : "out", dtype))) return rc;
   const int64_t pitch = act_pitch(cols);
-  if (rows * pitch > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^38 elements", fn);
+  if (rows * pitch > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
   const Buf bufs[] = {{x, rows * cols * dt_size(dtype), (int)dt_size(dtype), !pack, false, pack ? "x" : "out"},
                       {q, rows * pitch, 16, pack, false, "q"},
                       {scale, rows * (pitch / kActBlock), 1, pack, false, "scale"}};
@@ -253,7 +254,7 @@ static int wgrad_sizes(const char* fn, int64_t tokens, int64_t outs, int64_t ins
       (rc = check_size(fn, "ins", ins, 1, kMaxCols / 2)) || (rc = check_dtype(fn, "dy", dy_dtype)))
     return rc;
   if (outs * ins > ((int64_t)1 << 31)) return fail(MA_ERR_INVALID_ARG, "%s: outs * ins beyond 2^31", fn);
-  if (tokens * outs > kMaxElems || tokens * act_pitch(ins) > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^38 elements", fn);
+  if (tokens * outs > kMaxElems || tokens * act_pitch(ins) > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
   return MA_OK;
 }
 

@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(kBinThreads) k_embed_bin(const EmbedBwdArgs a)
 // backward, 2: the sums, a slice of 512 * CH columns per wave. A wave takes
 // kEmbedGroup consecutive slots, whose positions are consecutive in the sorted
 // order: it loads their counts and positions at once, sums each row's run (at
-// most kEmbedPiece tokens) and writes it, zeros for an empty one, or adds it to
+// most a.piece tokens) and writes it, zeros for an empty one, or adds it to
 // a row that occurs. Longer runs are summed by the piece waves (the launch's
-// first blocks), one per kEmbedPiece sorted positions: the part of a long run
+// first blocks), one per a.piece sorted positions: the part of a long run
 // that its first position belongs to goes to partial row 2p, that of another
 // long run that its last position belongs to to 2p + 1 (no third one fits), and
 // k_embed_join adds a run's parts in order.
@@ -301,17 +301,17 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int pie
   float acc[CH][8];
   if ((int)blockIdx.x < piece_blocks) {
     const int64_t p = (int64_t)blockIdx.x * 4 + wave;
-    const int64_t first = p * kEmbedPiece;
+    const int64_t first = p * a.piece;
     const int64_t left = *a.n_valid - first;
     if (left <= 0) return;
-    const int n = left < kEmbedPiece ? (int)left : kEmbedPiece;
+    const int n = left < a.piece ? (int)left : a.piece;
     const int32_t key = lane < n ? a.keys[first + lane] : 0, pos = lane < n ? a.order[first + lane] : 0;
     const int32_t va = __builtin_amdgcn_readlane(key, 0), vb = __builtin_amdgcn_readlane(key, n - 1);
     for (int side = 0; side < 2; ++side) {
       const int32_t v = side ? vb : va;
       if (side && vb == va) break;
       const int64_t s = a.start[v], c = a.count[v];
-      if (c <= kEmbedPiece) continue;
+      if (c <= a.piece) continue;
       const int from = s > first ? (int)(s - first) : 0;
       const int to = s + c - first < n ? (int)(s + c - first) : n;
       embed_sum<DD, CH>(a, pos, from, to, col, acc);
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int pie
     const int64_t v = ((int64_t)(bin0 + r) << a.log2nb) + owner;
     if (v >= a.rows) break;
     const int c = __builtin_amdgcn_readlane(counts, r);
-    if (c > kEmbedPiece || (ACC && c == 0)) continue;
+    if (c > a.piece || (ACC && c == 0)) continue;
     const int64_t s = __builtin_amdgcn_readlane(starts, r);
     const int32_t pos = lane < c ? a.order[s + lane] : 0;
     embed_sum<DD, CH>(a, pos, 0, c, col, acc);
@@ -353,11 +353,11 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdAr
   const int64_t mine = (int64_t)blockIdx.x * kJoinPieces + lane;
   bool starts = false;
   int32_t slot = 0, s = 0, c = 0;
-  if (lane < kJoinPieces && n_valid - mine * kEmbedPiece > kEmbedPiece) {
-    slot = a.keys[(mine + 1) * kEmbedPiece - 1];
+  if (lane < kJoinPieces && n_valid - mine * a.piece > a.piece) {
+    slot = a.keys[(mine + 1) * a.piece - 1];
     s = a.start[slot];
     c = a.count[slot];
-    starts = c > kEmbedPiece && s >= mine * kEmbedPiece;
+    starts = c > a.piece && s >= mine * a.piece;
   }
   const int col = blockIdx.y * 256 + lane * 4;
   const bool whole = col + 4 <= a.cols;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdAr
     const int i = __builtin_ctzll(todo);
     const int64_t p = (int64_t)blockIdx.x * kJoinPieces + i;
     const int64_t rs = __builtin_amdgcn_readlane(s, i), rc = __builtin_amdgcn_readlane(c, i);
-    const int64_t last = (rs + rc - 1) / kEmbedPiece;
+    const int64_t last = (rs + rc - 1) / a.piece;
     const int64_t n = last - p + 1, share = (n + kJoinWaves - 1) / kJoinWaves;
     const int64_t q0 = p + wave * share, q1 = q0 + share < last + 1 ? q0 + share : last + 1;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -373,13 +373,13 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdAr
     if (whole) {
 #pragma unroll 8
       for (int64_t q = q0; q < q1; ++q) {
-        const u32x4_t u = *reinterpret_cast<const V*>(a.partial + (2 * q + (q == p && rs > p * kEmbedPiece)) * a.cols + col);
+        const u32x4_t u = *reinterpret_cast<const V*>(a.partial + (2 * q + (q == p && rs > p * a.piece)) * a.cols + col);
         acc.x += __uint_as_float(u[0]); acc.y += __uint_as_float(u[1]); acc.z += __uint_as_float(u[2]); acc.w += __uint_as_float(u[3]);
       }
     } else if (col < a.cols) {
 #pragma unroll 8
       for (int64_t q = q0; q < q1; ++q) {
-        const float* src = a.partial + (2 * q + (q == p && rs > p * kEmbedPiece)) * a.cols;
+        const float* src = a.partial + (2 * q + (q == p && rs > p * a.piece)) * a.cols;
         // the row's end: columns past it repeat the last one, and are not stored
         acc.x += src[col]; acc.y += src[col + 1 < a.cols ? col + 1 : col]; acc.z += src[col + 2 < a.cols ? col + 2 : col];
       }
@@ -477,7 +477,7 @@ static int embed_log2nb(int64_t rows) {
   return log2nb;
 }
 static int64_t embed_per_block(int64_t rows) { return (rows + ((int64_t)1 << embed_log2nb(rows)) - 1) >> embed_log2nb(rows); }
-static int64_t embed_pieces(int64_t n_tokens) { return (n_tokens + kEmbedPiece - 1) / kEmbedPiece; }
+static int64_t embed_pieces(int64_t n_tokens) { return (n_tokens + embed_piece(n_tokens) - 1) / embed_piece(n_tokens); }
 
 size_t embed_bwd_workspace(int64_t rows, int64_t cols, int64_t n_tokens) {
   if (n_tokens <= kEmbedDirect) return 256;   // (not used; 0 would be an error)
@@ -488,6 +488,7 @@ size_t embed_bwd_workspace(int64_t rows, int64_t cols, int64_t n_tokens) {
 
 void embed_bwd_carve(EmbedBwdArgs& a, unsigned char* ws) {
   a.log2nb = embed_log2nb(a.rows);
+  a.piece = embed_piece(a.n_tokens);
   a.per_block = (int32_t)embed_per_block(a.rows);
   const int64_t slots = (int64_t)a.per_block << a.log2nb;
   auto take = [&](int64_t bytes) { unsigned char* p = ws; ws += round_up(bytes, 256); return p; };

@@ -350,8 +350,8 @@ int ma_lion_step(const ma_lion_segment* segments, int32_t n_segments, void* stre
  * tokens: n_tokens integers of token_bytes (4 or 8, signed); out: n_tokens x
  * cols. A token outside 0..rows-1 is ignored: its output row is zero, and it
  * takes no part in the gradient (a row of another rank's shard, a masked
- * position). Limits: rows, cols <= 2^24, n_tokens <= 2^25, rows * cols and
- * n_tokens * cols <= 2^38; scale finite. */
+ * position). Limits: rows <= 2^24, cols <= 2^20, n_tokens <= 2^25, rows * cols
+ * and n_tokens * cols <= 2^36; scale finite. */
 int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, int64_t cols, const void* tokens,
                          int32_t token_bytes, int64_t n_tokens, float scale, void* out, int32_t out_dtype, void* stream);
 
@@ -359,15 +359,16 @@ int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, i
  * every row v < rows (zero where there is none). With accumulate the rows that
  * occur are added to and no other row is touched. dout: n_tokens x cols; grad:
  * rows x cols, fp32. The tokens are sorted first (stable, by kernels of this
- * call): runs of up to 64 are summed in ascending i, longer ones in pieces that
- * are joined in order. workspace: at least ma_embedding_workspace_size bytes
+ * call): short runs are summed in ascending i, longer ones in pieces that are
+ * joined in order. workspace: at least ma_embedding_workspace_size bytes
  * (0 from that function: invalid sizes), MA_WORKSPACE_ALIGN aligned. */
 size_t ma_embedding_workspace_size(int64_t rows, int64_t cols, int64_t n_tokens);
 int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* tokens, int32_t token_bytes, int64_t n_tokens,
                           int64_t rows, int64_t cols, float scale, int32_t accumulate, float* grad, void* workspace,
                           size_t workspace_bytes, void* stream);
 
-/* Layer norm over the last dimension, per row of x (rows x cols, cols <= 16384):
+/* Layer norm over the last dimension, per row of x (rows x cols; rows <= 2^24,
+ * cols <= 16384, rows * cols <= 2^36):
  *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
  *   y = (x - mean) * rstd * gain + bias        gain, bias: cols fp32 values, either may be null
  * stats (rows x 2 fp32, 8-byte aligned) receives mean and rstd for the backward
@@ -400,7 +401,8 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
  * every value held is finite in bf16 and fp32). NaN and infinities are held as
  * NaN. Every held value is exact in bf16: unpacking rounds nothing, and the
  * error against x is at most 2^-4 |x|, or 2^-10 * 2^e for values below the
- * block's e4m3 normal range (2^-6 * 2^e). */
+ * block's e4m3 normal range (2^-6 * 2^e). Limits: rows, cols <= 2^24, rows * P
+ * <= 2^36. */
 #define MA_ACT_BLOCK 128
 int ma_act_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, uint8_t* q, uint8_t* scale, void* stream);
 int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, void* out, int32_t out_dtype,
@@ -411,7 +413,8 @@ int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
  * dy: tokens x outs; q, scale: the checkpoint of x (tokens x ins) as written by
  * ma_act_pack; grad: outs x ins. The held values are used as they are (no
  * second rounding) and dy at its full precision; products are summed in fp32.
- * Limits: tokens <= 2^25, outs, ins <= 2^23, outs * ins <= 2^31. workspace: at
+ * Limits: tokens <= 2^25, outs, ins <= 2^23, outs * ins <= 2^31, tokens * outs and
+ * tokens * P <= 2^36. workspace: at
  * least ma_act_weight_grad_workspace_size bytes, which may be 0. */
 size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype);
 int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const uint8_t* scale, int64_t tokens,
