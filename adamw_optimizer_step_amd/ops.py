@@ -57,7 +57,7 @@ def _launch(dev: torch.device, stream, go):
     """``go(raw stream)`` with the tensors' device current and, where a stream is
     given, that stream too, so that what ``go`` allocates belongs to it."""
     if stream is None:
-        if torch.cuda.current_device() == dev.index:
+        if torch._C._cuda_getDevice() == dev.index:
             return go(torch._C._cuda_getCurrentRawStream(dev.index))
         with torch.cuda.device(dev):
             return go(torch._C._cuda_getCurrentRawStream(dev.index))
@@ -152,17 +152,19 @@ def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, grad: torch.Ten
 class ActCheckpoint:
     """An activation matrix ``[rows, cols]`` held in 8 bits: ``q`` (uint8
     ``[rows, P]``, P = cols rounded up to a multiple of 128) and ``scale``
-    (uint8 ``[rows, P / 128]``), as ``act_pack`` writes them."""
+    (uint8 ``[rows, P / 128]``), as ``act_pack`` writes them. ``empty`` keeps
+    both in one allocation."""
 
-    __slots__ = ("q", "scale", "rows", "cols")
+    __slots__ = ("rows", "cols", "_tensors", "_q", "_scale")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int):
         blocks = -(-int(cols) // L.MA_ACT_BLOCK)
         if cols < 1:
             raise ValueError("a checkpoint has at least one column")
         rows = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 2 else -1
-        self.q = _check("q", q, (torch.uint8,), (rows, blocks * L.MA_ACT_BLOCK))
-        self.scale = _check("scale", scale, (torch.uint8,), (rows, blocks))
+        self._q = _check("q", q, (torch.uint8,), (rows, blocks * L.MA_ACT_BLOCK))
+        self._scale = _check("scale", scale, (torch.uint8,), (rows, blocks))
+        self._tensors = (q, scale)
         self.rows, self.cols = rows, int(cols)
 
     @classmethod
@@ -170,15 +172,37 @@ class ActCheckpoint:
         """Room for the checkpoint of a ``[rows, cols]`` matrix."""
         if rows < 0 or cols < 1:
             raise ValueError(f"no checkpoint of {rows} rows and {cols} columns")
-        blocks = -(-cols // L.MA_ACT_BLOCK)
         self = cls.__new__(cls)
-        self.q = torch.empty((rows, blocks * L.MA_ACT_BLOCK), dtype=torch.uint8, device=device)
-        self.scale = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
         self.rows, self.cols = rows, cols
+        self._tensors = (torch.empty(rows * (-(-cols // L.MA_ACT_BLOCK)) * (L.MA_ACT_BLOCK + 1), dtype=torch.uint8, device=device),)
+        self._q = self._scale = None
         return self
 
+    def _views(self) -> None:
+        blocks = -(-self.cols // L.MA_ACT_BLOCK)
+        n = self.rows * blocks * L.MA_ACT_BLOCK
+        self._q = self._tensors[0][:n].view(self.rows, blocks * L.MA_ACT_BLOCK)
+        self._scale = self._tensors[0][n:].view(self.rows, blocks)
+
+    @property
+    def q(self) -> torch.Tensor:
+        if self._q is None:
+            self._views()
+        return self._q
+
+    @property
+    def scale(self) -> torch.Tensor:
+        if self._scale is None:
+            self._views()
+        return self._scale
+
     def nbytes(self) -> int:
-        return self.q.numel() + self.scale.numel()
+        return self.rows * (-(-self.cols // L.MA_ACT_BLOCK)) * (L.MA_ACT_BLOCK + 1)
+
+    def _pointers(self) -> Tuple[int, int]:
+        t = self._tensors
+        p = t[0].data_ptr()
+        return p, t[1].data_ptr() if len(t) == 2 else p + self.rows * (-(-self.cols // L.MA_ACT_BLOCK)) * L.MA_ACT_BLOCK
 
 
 def _check_checkpoint(what: str, c: "ActCheckpoint", rows: int, cols: int) -> "ActCheckpoint":
@@ -196,13 +220,13 @@ def act_pack(x: torch.Tensor, out: Optional[ActCheckpoint] = None, stream=None) 
     rows, cols = _rows("x", x)
     if out is not None:
         _check_checkpoint("out", out, rows, cols)
-    dev = _device(x, out.q, out.scale) if out is not None else _device(x)
+    dev = _device(x, *out._tensors) if out is not None else _device(x)
 
     def go(s):
         nonlocal out
         if out is None:
             out = ActCheckpoint.empty(rows, cols, dev)
-        L.check(L.lib().ma_act_pack(x.data_ptr(), _dt(x), rows, cols, out.q.data_ptr(), out.scale.data_ptr(), s))
+        L.check(L.lib().ma_act_pack(x.data_ptr(), _dt(x), rows, cols, *out._pointers(), s))
         return out
     return _launch(dev, stream, go)
 
@@ -220,13 +244,13 @@ def act_unpack(checkpoint: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, o
             raise ValueError(f"out: expected {rows} rows of {cols} columns, got {tuple(out.shape)}")
     elif dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
-    dev = _device(checkpoint.q, checkpoint.scale, out)
+    dev = _device(*checkpoint._tensors, out)
 
     def go(s):
         nonlocal out
         if out is None:
             out = torch.empty((rows, cols), dtype=dtype, device=dev)
-        L.check(L.lib().ma_act_unpack(checkpoint.q.data_ptr(), checkpoint.scale.data_ptr(), rows, cols, out.data_ptr(), _dt(out), s))
+        L.check(L.lib().ma_act_unpack(*checkpoint._pointers(), rows, cols, out.data_ptr(), _dt(out), s))
         return out
     return _launch(dev, stream, go)
 
@@ -257,19 +281,18 @@ def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     if stats is not None:
         _check("stats", stats, (torch.float32,), (rows, 2))
-    q = sc = None
-    if checkpoint is not None:
-        q, sc = _check_checkpoint("checkpoint", checkpoint, rows, cols).q, checkpoint.scale
-    dev = _device(x, gain, bias, out, stats, q, sc)
+    held = () if checkpoint is None else _check_checkpoint("checkpoint", checkpoint, rows, cols)._tensors
+    dev = _device(x, gain, bias, out, stats, *held)
 
     def go(s):
         nonlocal out, stats
         if out is None:
-            out = torch.empty(x.shape, dtype=dtype or x.dtype, device=dev)
+            out = torch.empty_like(x) if dtype is None or dtype == x.dtype else torch.empty(x.shape, dtype=dtype, device=dev)
         if stats is None:
             stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        q, sc = checkpoint._pointers() if checkpoint is not None else (None, None)
         L.check(L.lib().ma_layernorm_forward(x.data_ptr(), _dt(x), rows, cols, _ptr(gain), _ptr(bias), eps, out.data_ptr(), _dt(out),
-                                             stats.data_ptr(), _ptr(q), _ptr(sc), s))
+                                             stats.data_ptr(), q, sc, s))
         return out, stats
     return _launch(dev, stream, go)
 
@@ -295,10 +318,10 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
     rows, cols = _rows("dy", dy)
     if isinstance(x, ActCheckpoint):
         _check_checkpoint("x", x, rows, cols)
-        xt, q, sc, dx_dtype, xd = None, x.q, x.scale, dy.dtype, 0
+        xt, held, dx_dtype, xd = None, x._tensors, dy.dtype, 0
     else:
         _check("x", x, _DT, dy.shape)
-        xt, q, sc, dx_dtype, xd = x, None, None, x.dtype, _dt(x)
+        xt, held, dx_dtype, xd = x, (), x.dtype, _dt(x)
     _check("stats", stats, (torch.float32,), (rows, 2))
     _param("gain", gain, cols)
     _param("dgain", dgain, cols)
@@ -306,16 +329,17 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
     if dx is not None:
         _check("dx", dx, (dx_dtype,), dy.shape)
     _check_workspace(workspace)
-    dev = _device(dy, xt, q, sc, stats, gain, dgain, dbias, dx, workspace)
+    dev = _device(dy, xt, *held, stats, gain, dgain, dbias, dx, workspace)
     sums = dgain is not None or dbias is not None
 
     def go(s):
         nonlocal dx
         if dx is None:
-            dx = torch.empty(dy.shape, dtype=dx_dtype, device=dev)
+            dx = torch.empty_like(dy if xt is None else xt)
+        q, sc = x._pointers() if held else (None, None)
         need = layernorm_workspace_size(rows, cols) if sums else 0
         ws = _workspace(workspace, need, dev) if need or workspace is not None else None
-        L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, _ptr(q), _ptr(sc), rows, cols, stats.data_ptr(),
+        L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, q, sc, rows, cols, stats.data_ptr(),
                                               _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
                                               _ptr(ws), ws.numel() if ws is not None else 0, s))
         return dx
@@ -349,12 +373,12 @@ def act_weight_grad(dy: torch.Tensor, x: ActCheckpoint, grad: torch.Tensor, accu
         raise ValueError(f"dy has {tokens} rows, the checkpoint {x.rows}")
     _check("grad", grad, _DT, (outs, x.cols))
     _check_workspace(workspace)
-    dev = _device(dy, x.q, x.scale, grad, workspace)
+    dev = _device(dy, *x._tensors, grad, workspace)
 
     def go(s):
         need = act_weight_grad_workspace_size(tokens, outs, x.cols, dy.dtype)
         ws = _workspace(workspace, need, dev) if need or workspace is not None else None
-        L.check(L.lib().ma_act_weight_grad(dy.data_ptr(), _dt(dy), x.q.data_ptr(), x.scale.data_ptr(), tokens, outs, x.cols,
+        L.check(L.lib().ma_act_weight_grad(dy.data_ptr(), _dt(dy), *x._pointers(), tokens, outs, x.cols,
                                            grad.data_ptr(), _dt(grad), int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0, s))
         return grad
     return _launch(dev, stream, go)
