@@ -258,14 +258,13 @@ static int wgrad_sizes(const char* fn, int64_t tokens, int64_t outs, int64_t ins
   return MA_OK;
 }
 
-static size_t wgrad_workspace(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype) {
-  const int splits = wgrad_splits(tokens, outs, ins, dy_dtype);
+static size_t wgrad_workspace(int splits, int64_t outs, int64_t ins) {
   return splits > 1 ? (size_t)(splits * wgrad_partial(outs, ins) * 4) : 0;
 }
 
 size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype) {
   if (wgrad_sizes("ma_act_weight_grad_workspace_size", tokens, outs, ins, dy_dtype)) return 0;
-  return wgrad_workspace(tokens, outs, ins, dy_dtype);
+  return wgrad_workspace(wgrad_plan(tokens, outs, ins, dy_dtype).splits, outs, ins);
 }
 
 int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const uint8_t* scale, int64_t tokens, int64_t outs, int64_t ins,
@@ -275,7 +274,8 @@ int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const
   int rc;
   if ((rc = wgrad_sizes(fn, tokens, outs, ins, dy_dtype)) || (rc = check_dtype(fn, "grad", grad_dtype)) || (rc = check_flag(fn, accumulate))) return rc;
   const int64_t pitch = act_pitch(ins);
-  const size_t need = wgrad_workspace(tokens, outs, ins, dy_dtype);
+  const WgradPlan plan = wgrad_plan(tokens, outs, ins, dy_dtype);
+  const size_t need = wgrad_workspace(plan.splits, outs, ins);
   const Buf bufs[] = {{dy, tokens * outs * dt_size(dy_dtype), (int)dt_size(dy_dtype), false, false, "dy"},
                       {q, tokens * pitch, 16, false, false, "q"},
                       {scale, tokens * (pitch / kActBlock), 1, false, false, "scale"},
@@ -286,7 +286,7 @@ int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const WgradArgs a{dy, q, scale, grad, reinterpret_cast<float*>(workspace), tokens, (int32_t)outs, (int32_t)ins, accumulate,
-                    wgrad_splits(tokens, outs, ins, dy_dtype)};
+                    plan.splits, plan.big};
   ProfScope ps(MA_K_WEIGHT_GRAD, s);
   return done(launch_wgrad(a, dy_dtype, grad_dtype, s), fn);
 }

@@ -24,8 +24,11 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hip
 // longest wave, long ones the join (5003 tokens x 333 fp32: sums 7.5 us with 16,
 // 10.5 with 32, join 4.2 both; 49152 x 1024 bf16: sums 68 both, join 10.3 and 7.3).
 constexpr int embed_piece(int64_t n_tokens) { return n_tokens <= 16384 ? 16 : 32; }
-// Up to this many tokens the rows' waves look for their tokens themselves.
-constexpr int kEmbedDirect = 512;
+// Up to this many tokens the rows' waves look for their tokens themselves, in
+// one launch in place of three (bf16 into 1000 x 1024: 1000 tokens 15 us against
+// 5.8 + 8.5 + 3.7 and two launches, 2000 tokens 24 against 6 + 8.2 + 4.6; into
+// 50304 x 1024: 35 against 6 + 37 + 4.7).
+constexpr int kEmbedDirect = 1024;
 struct EmbedBwdArgs {
   const void* dout;
   const void* tokens;
@@ -92,11 +95,12 @@ struct WgradArgs {
   void* grad;                 // outs x ins
   float* partial;             // [splits][wgrad_partial], splits > 1
   int64_t tokens;
-  int32_t outs, ins, accumulate, splits;
+  int32_t outs, ins, accumulate, splits, big;   // splits, big: wgrad_plan's
 };
+struct WgradPlan { bool big; int splits; };
 // elements of one split's partial products (whole cache lines)
 __host__ __device__ constexpr int64_t wgrad_partial(int64_t outs, int64_t ins) { return round_up(outs * ins, 64); }
-int wgrad_splits(int64_t tokens, int64_t outs, int64_t ins, int dy_dt);
+WgradPlan wgrad_plan(int64_t tokens, int64_t outs, int64_t ins, int dy_dt);
 hipError_t launch_wgrad(const WgradArgs& a, int dy_dt, int grad_dt, hipStream_t s);
 
 }  // namespace ma

@@ -392,15 +392,13 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const WgradArgs a) {
   }
 }
 
-struct WgradPlan { bool big; int splits; };
-
 // Tile and number of splits by the time they should take (us), from what single
 // launches of 64 .. 4096 tokens took: a fixed part, the k-tiles of the blocks
 // that share a CU (one or two small tiles, one big one, slower as more CUs draw
 // on memory and power), the outputs or partial products written, and the join.
 //   k-tile of 64 tokens, bf16 dy: 128 x 128 0.66 alone, 1.08 for a pair; 256 x 256 1.2 (64 blocks) to 1.6 (256)
 //   k-tile of 32 tokens, fp32 dy: 0.92, 1.5; 1.75 to 2.3
-static WgradPlan wgrad_plan(int64_t tokens, int64_t outs, int64_t ins, int dy_dt) {
+WgradPlan wgrad_plan(int64_t tokens, int64_t outs, int64_t ins, int dy_dt) {
   const bool f32 = dy_dt == DT_F32;
   const int64_t bk = f32 ? 32 : 64, vt = (tokens + bk - 1) / bk;
   const double mb = (double)outs * (double)ins * 4e-6;   // of one fp32 result
@@ -421,8 +419,6 @@ static WgradPlan wgrad_plan(int64_t tokens, int64_t outs, int64_t ins, int dy_dt
   return best;
 }
 
-int wgrad_splits(int64_t tokens, int64_t outs, int64_t ins, int dy_dt) { return wgrad_plan(tokens, outs, ins, dy_dt).splits; }
-
 template <int DYD, int GD, typename TL>
 static hipError_t wgrad_tile(const WgradArgs& a, hipStream_t s) {
   const int64_t jobs = (int64_t)((a.outs + TL::BM - 1) / TL::BM) * ((a.ins + TL::BN - 1) / TL::BN) * a.splits;
@@ -436,7 +432,7 @@ static hipError_t wgrad_tile(const WgradArgs& a, hipStream_t s) {
 
 template <int DYD, int GD>
 static hipError_t wgrad(const WgradArgs& a, hipStream_t s) {
-  return wgrad_plan(a.tokens, a.outs, a.ins, DYD).big ? wgrad_tile<DYD, GD, wg::Big<DYD>>(a, s) : wgrad_tile<DYD, GD, wg::Small<DYD>>(a, s);
+  return a.big ? wgrad_tile<DYD, GD, wg::Big<DYD>>(a, s) : wgrad_tile<DYD, GD, wg::Small<DYD>>(a, s);
 }
 
 hipError_t launch_wgrad(const WgradArgs& a, int dy_dt, int grad_dt, hipStream_t s) {

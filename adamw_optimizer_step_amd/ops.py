@@ -300,7 +300,7 @@ def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias
 def layernorm_workspace_size(rows: int, cols: int) -> int:
     """Bytes of workspace (0: none needed)."""
     n = L.lib().ma_layernorm_workspace_size(rows, cols)
-    if n == 0 and not (0 <= rows <= 1 << 24 and 1 <= cols <= 16384):
+    if n == 0 and not (0 <= rows <= 1 << 24 and 1 <= cols <= 16384 and rows * cols <= 1 << 36):
         L.check(L.MA_ERR_INVALID_ARG)
     return int(n)
 
@@ -354,7 +354,8 @@ def act_weight_grad_workspace_size(tokens: int, outs: int, ins: int, dtype: torc
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     n = L.lib().ma_act_weight_grad_workspace_size(tokens, outs, ins, _DT[dtype])
-    if n == 0 and (min(outs, ins) < 1 or tokens < 0):
+    if n == 0 and not (0 <= tokens <= 1 << 25 and 1 <= outs <= 1 << 23 and 1 <= ins <= 1 << 23 and outs * ins <= 1 << 31
+                       and tokens * max(outs, -(-ins // L.MA_ACT_BLOCK) * L.MA_ACT_BLOCK) <= 1 << 36):
         L.check(L.MA_ERR_INVALID_ARG)
     return int(n)
 

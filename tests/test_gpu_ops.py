@@ -119,6 +119,8 @@ def test_embedding_shapes_and_defaults():
     (200000, 5, 2500, F32, "spread", 0), (40, 24, 100, F32, "none", 0), (3, 16, 20000, F32, "spread", 0),
     (70, 520, 512, BF16, "one", 0), (70, 520, 513, BF16, "one", 0), (9, 33, 511, F32, "outside", 1), (9, 33, 700, F32, "none", 0),
     (1 << 18, 3, 600, F32, "zipf", 0), (513, 8, 17000, BF16, "zipf", 0),
+    (70, 520, 1024, BF16, "one", 0), (70, 520, 1025, BF16, "one", 0), (700, 2050, 1025, F32, "outside", 0), (9, 33, 1023, F32, "outside", 1),
+    (40, 1033, 900, F32, "zipf", 1), (9, 33, 1100, F32, "none", 0), (1 << 18, 3, 1300, F32, "zipf", 0), (3, 8, 300000, BF16, "zipf", 0),
 ])
 @pytest.mark.parametrize("acc", [False, True])
 def test_embedding_backward(rows, cols, n, dd, kind, off, acc):
@@ -272,6 +274,17 @@ def test_layernorm_without_rows():
     assert ma.layernorm_backward(y, x, stats, dgain=dg, accumulate=True).shape == (0, 64) and bool((dg == 1).all())
     ma.layernorm_backward(y, x, stats, dgain=dg)
     assert not dg.any()
+
+
+@pytest.mark.parametrize("eps", [1e-40, 1e-30])
+def test_layernorm_of_equal_values_with_a_tiny_eps(eps):
+    """A row of equal values has no variance: y is the bias and rstd 1 / sqrt(eps), also where eps is subnormal."""
+    x, b = torch.full((5, 256), 0.5, device=DEV), rand((256,), 44)
+    y, stats = ma.layernorm_forward(x, bias=b, eps=eps)
+    assert torch.equal(y, b.expand(5, 256))
+    want = 1.0 / np.sqrt(float(np.float32(eps)))
+    # the reciprocal root is good to 2 units in the last place
+    close(stats[:, 1], np.full(5, want), 4 * U * want)
 
 
 def test_layernorm_nonfinite_rows_stay_in_their_row():

@@ -107,7 +107,9 @@ def test_workspace_sizes():
     assert ma.layernorm_workspace_size(0, 64) == 0 and ma.layernorm_workspace_size(1, 64) == 0 and ma.layernorm_workspace_size(5000, 64) >= 2 * 64 * 4
     assert ma.act_weight_grad_workspace_size(0, 4, 4) == 0
     for f, a in ((ma.embedding_workspace_size, (0, 1, 1)), (ma.layernorm_workspace_size, (5, 1 << 20)),
-                 (ma.act_weight_grad_workspace_size, (5, 0, 3))):
+                 (ma.act_weight_grad_workspace_size, (5, 0, 3)), (ma.layernorm_workspace_size, (1 << 24, 16384)),
+                 (ma.act_weight_grad_workspace_size, (1 << 26, 4, 4)), (ma.act_weight_grad_workspace_size, (5, 1 << 24, 4)),
+                 (ma.act_weight_grad_workspace_size, (5, 1 << 20, 1 << 20)), (ma.act_weight_grad_workspace_size, (1 << 20, 4, 1 << 20))):
         with pytest.raises(ma.MuonAdamWError):
             f(*a)
 
