@@ -15,7 +15,7 @@ namespace {
 // size limits: keep every launch within 2^32 threads and every index within its type
 constexpr int64_t kMaxRows = (int64_t)1 << 24, kMaxCols = (int64_t)1 << 24, kMaxTokens = (int64_t)1 << 25;
 constexpr int64_t kMaxEmbedCols = (int64_t)1 << 20;
-constexpr int64_t kMaxElems = (int64_t)1 << 36;
+constexpr int64_t kMaxElems = (int64_t)1 << 36, kMaxTable = (int64_t)1 << 35;   // (a wave per row and 1024 columns of the table)
 
 bool dt_ok(int dt) { return dt == MA_F32 || dt == MA_BF16; }
 int64_t dt_size(int dt) { return dt == MA_BF16 ? 2 : 4; }
@@ -84,6 +84,7 @@ int done(hipError_t err, const char* fn) { return err == hipSuccess ? MA_OK : hi
 int embedding_sizes(const char* fn, int64_t rows, int64_t cols, int64_t n_tokens) {
   int rc;
   if ((rc = check_matrix(fn, rows, 1, kMaxRows, cols, kMaxEmbedCols)) || (rc = check_size(fn, "n_tokens", n_tokens, 0, kMaxTokens))) return rc;
+  if (rows * cols > kMaxTable) return fail(MA_ERR_INVALID_ARG, "%s: a table of more than 2^35 elements", fn);
   if (n_tokens * cols > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
   return MA_OK;
 }

@@ -351,7 +351,7 @@ int ma_lion_step(const ma_lion_segment* segments, int32_t n_segments, void* stre
  * cols. A token outside 0..rows-1 is ignored: its output row is zero, and it
  * takes no part in the gradient (a row of another rank's shard, a masked
  * position). Limits: rows <= 2^24, cols <= 2^20, n_tokens <= 2^25, rows * cols
- * and n_tokens * cols <= 2^36; scale finite. */
+ * <= 2^35, n_tokens * cols <= 2^36; scale finite. */
 int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, int64_t cols, const void* tokens,
                          int32_t token_bytes, int64_t n_tokens, float scale, void* out, int32_t out_dtype, void* stream);
 

@@ -43,7 +43,7 @@ def call(name, **kw):
 BAD = [
     ("ma_embedding_forward", dict(rows=0), INV), ("ma_embedding_forward", dict(cols=0), INV),
     ("ma_embedding_forward", dict(rows=(1 << 24) + 1), INV), ("ma_embedding_forward", dict(cols=(1 << 24) + 1), INV),
-    ("ma_embedding_forward", dict(rows=1 << 24, cols=1 << 15), INV), ("ma_embedding_forward", dict(n_tokens=-1), INV),
+    ("ma_embedding_forward", dict(rows=1 << 24, cols=1 << 15), INV), ("ma_embedding_forward", dict(rows=1 << 24, cols=2049), INV), ("ma_embedding_forward", dict(n_tokens=-1), INV),
     ("ma_embedding_forward", dict(n_tokens=(1 << 25) + 1), INV), ("ma_embedding_forward", dict(table_dtype=2), UNS),
     ("ma_embedding_forward", dict(out_dtype=-1), UNS), ("ma_embedding_forward", dict(token_bytes=2), UNS),
     ("ma_embedding_forward", dict(scale=float("nan")), INV), ("ma_embedding_forward", dict(table=None), INV),
