@@ -371,10 +371,18 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdAr
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     typedef typename U16<DT_F32>::T V;
     if (whole) {
-#pragma unroll 8
-      for (int64_t q = q0; q < q1; ++q) {
-        const u32x4_t u = *reinterpret_cast<const V*>(a.partial + (2 * q + (q == p && rs > p * a.piece)) * a.cols + col);
-        acc.x += __uint_as_float(u[0]); acc.y += __uint_as_float(u[1]); acc.z += __uint_as_float(u[2]); acc.w += __uint_as_float(u[3]);
+      constexpr int U = 8;   // parts in flight
+      for (int64_t q = q0; q < q1; q += U) {
+        u32x4_t x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[u] = u32x4_t{0u, 0u, 0u, 0u};
+          if (q + u < q1) x[u] = *reinterpret_cast<const V*>(a.partial + (2 * (q + u) + (q + u == p && rs > p * a.piece)) * a.cols + col);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          acc.x += __uint_as_float(x[u][0]); acc.y += __uint_as_float(x[u][1]); acc.z += __uint_as_float(x[u][2]); acc.w += __uint_as_float(x[u][3]);
+        }
       }
     } else if (col < a.cols) {
 #pragma unroll 8

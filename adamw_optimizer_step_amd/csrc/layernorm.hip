@@ -140,17 +140,32 @@ __device__ __forceinline__ void norm_cols_direct(const NormBwdArgs& a, int tile,
   const int64_t pitch = act_pitch(a.cols);
   float dg = 0.0f, db = 0.0f;
   if (col < a.cols) {
-#pragma unroll 16
-    for (int row = wave; row < (int)a.rows; row += W) {
-      float x;
-      if constexpr (XD == DT_ACT8)
-        x = __builtin_amdgcn_cvt_f32_fp8(a.q[row * pitch + col], 0) * act_scale(a.qscale[row * (pitch / kActBlock) + col / kActBlock]);
-      else
-        x = load1<raw_dt<XD>()>(a.x, (int64_t)row * a.cols + col);
-      const float d = load1<DYD>(a.dy, (int64_t)row * a.cols + col);
-      dg = __builtin_fmaf(d, (x - a.stats[2 * row]) * a.stats[2 * row + 1], dg);
-      db += d;
-    }
+    // U rows in flight as long as so many are left
+    int row = wave;
+    auto rows_by = [&](auto n) __attribute__((always_inline)) {
+      constexpr int U = decltype(n)::value;
+      for (; row + (U - 1) * W < (int)a.rows; row += U * W) {
+        float x[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = row + u * W;
+          if constexpr (XD == DT_ACT8)
+            x[u] = __builtin_amdgcn_cvt_f32_fp8(a.q[r * pitch + col], 0) * act_scale(a.qscale[r * (pitch / kActBlock) + col / kActBlock]);
+          else
+            x[u] = load1<raw_dt<XD>()>(a.x, (int64_t)r * a.cols + col);
+          d[u] = load1<DYD>(a.dy, (int64_t)r * a.cols + col);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = row + u * W;
+          dg = __builtin_fmaf(d[u], (x[u] - a.stats[2 * r]) * a.stats[2 * r + 1], dg);
+          db += d[u];
+        }
+      }
+    };
+    rows_by(std::integral_constant<int, 16>());
+    rows_by(std::integral_constant<int, 4>());
+    rows_by(std::integral_constant<int, 1>());
   }
   part[wave][0][lane] = dg;
   part[wave][1][lane] = db;
@@ -170,6 +185,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(G)) k_norm_bwd(const NormBwdA
   __shared__ float join[ROWS > 1 ? ROWS / 2 : 1][ROWS > 1 ? G * CH * 8 : 1];
   if constexpr (DIRECT) {
     __shared__ float cols[W][2][64];
+    // (the last blocks: first, they would read columns past cold caches; 512 x 1024 bf16 8.2 us against 4.9)
     if ((int)blockIdx.x >= a.blocks) {
       norm_cols_direct<XD, DYD, W>(a, (int)blockIdx.x - a.blocks, cols);
       return;
@@ -334,8 +350,12 @@ __global__ void __launch_bounds__(1024) k_norm_cols(const NormBwdArgs a) {
   const int share = (a.blocks + 31) / 32, b0 = group * share, b1 = b0 + share < a.blocks ? b0 + share : a.blocks;
   float v = 0.0f;
   const float* src = a.partial + (int64_t)blockIdx.y * round_up(a.cols, 32) * a.blocks + (int64_t)blockIdx.x * a.blocks * 32 + lane;
-#pragma unroll 16
-  for (int b = b0; b < b1; ++b) v += src[b * 32];
+  constexpr int U = 16;   // a share is no longer (norm_bwd_blocks)
+  float x[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) x[u] = b0 + u < b1 ? src[(b0 + u) * 32] : 0.0f;
+#pragma unroll
+  for (int u = 0; u < U; ++u) v += x[u];
   part[group][lane] = v;
   __syncthreads();
   if (group == 0 && col < a.cols) {
@@ -404,14 +424,16 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dt, int y_dt, hipStream_t
   return y_dt == DT_F32 ? norm_fwd<DT_BF16, DT_F32>(a, s) : norm_fwd<DT_BF16, DT_BF16>(a, s);
 }
 
-// Whether the rows are so few that no partial sums are kept.
-constexpr int64_t kNormDirectRows = 512;
+// Whether the rows are so few that no partial sums are kept: reading x and dy
+// again costs less than a launch more (bf16 of 1024 columns: 513 rows 4.9 us in one
+// launch, 4.9 + 3 in two; 1000 rows 8.1 and 5.2 + 3.3; 2000 rows 17 and 6.9 + 3.5).
+constexpr int64_t kNormDirectRows = 1024;
 bool norm_bwd_direct(int64_t rows) { return rows <= kNormDirectRows; }
 
 // As many as are resident at once (16 waves per CU); where a row takes 256 lanes
 // or more at least 4 steps each, down to 128 blocks: every block writes, and
 // k_norm_cols reads, two rows of sums (1537 x 2047, fp32 dy: 11 + 4.3 us with 193
-// blocks, 12.4 + 3.9 with 385; 500 x 4096: 11.6 + 3.8 with 128, 13.2 + 5 with 500).
+// blocks, 12.4 + 3.9 with 385).
 int norm_bwd_blocks(int64_t rows, int64_t cols) {
   int64_t units = rows, most = 0;
   bool wide = false;
@@ -419,6 +441,7 @@ int norm_bwd_blocks(int64_t rows, int64_t cols) {
     constexpr int G = decltype(sh)::G, T = norm_bwd_threads(G);
     units = (rows + T / G - 1) / (T / G);
     most = 256 * 16 * 64 / T;
+    static_assert(256 * 16 * 64 / T <= 32 * 16, "k_norm_cols' shares");
     wide = G >= 256;
     return hipSuccess;
   });

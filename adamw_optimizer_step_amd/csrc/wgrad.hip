@@ -378,11 +378,18 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const WgradArgs a) {
   float v[4] = {};
   const int n = total - i < 4 ? (int)(total - i) : 4;
   const int64_t stride = wgrad_partial(a.outs, a.ins);   // past the end there is room, not read further
-#pragma unroll 8
-  for (int s = 0; s < a.splits; ++s) {
-    const u32x4_t u = *reinterpret_cast<const u32x4_t*>(a.partial + s * stride + i);
+  constexpr int U = 8;
+  for (int s = 0; s < a.splits; s += U) {
+    u32x4_t x[U];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += __uint_as_float(u[e]);
+    for (int u = 0; u < U; ++u) {
+      x[u] = u32x4_t{0u, 0u, 0u, 0u};
+      if (s + u < a.splits) x[u] = *reinterpret_cast<const u32x4_t*>(a.partial + (s + u) * stride + i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += __uint_as_float(x[u][e]);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

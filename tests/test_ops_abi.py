@@ -68,7 +68,7 @@ BAD = [
     ("ma_layernorm_backward", dict(x=None), INV), ("ma_layernorm_backward", dict(x=None, ckpt_q=at(8)), INV),
     ("ma_layernorm_backward", dict(ckpt_q=at(8), ckpt_scale=at(9)), INV), ("ma_layernorm_backward", dict(stats=None), INV),
     ("ma_layernorm_backward", dict(dx=at(0)), INV), ("ma_layernorm_backward", dict(dgain=at(6)), INV),
-    ("ma_layernorm_backward", dict(rows=1000, workspace=None), WS), ("ma_layernorm_backward", dict(rows=1000, workspace_bytes=8), WS),
+    ("ma_layernorm_backward", dict(rows=1100, workspace=None), WS), ("ma_layernorm_backward", dict(rows=1100, workspace_bytes=8), WS),
     ("ma_layernorm_backward", dict(accumulate=-1), INV),
     ("ma_layernorm_backward", dict(x=None, ckpt_q=at(8), ckpt_scale=at(9), dy_dtype=0, dx_dtype=1), UNS),
     ("ma_act_pack", dict(x=None), INV), ("ma_act_pack", dict(q=at(1) + 4), INV), ("ma_act_pack", dict(q=at(0)), INV),
