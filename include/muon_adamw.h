@@ -22,6 +22,10 @@
  *                  exercise 5; "Muon vs AdamW, Lion and Sophia: a fair
  *                  race", section "Lion").
  *
+ * and the operators that fill the gradients they read: ma_embedding_*,
+ * ma_layernorm_*, ma_act_* (8-bit activation checkpoints and the weight
+ * gradient of a linear layer out of one).
+ *
  * Conventions for every entry point:
  *   - Pointers named "device" are HIP device pointers; "host" pointers are
  *     read during the call only and may be freed when it returns.

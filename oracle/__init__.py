@@ -18,6 +18,9 @@ nothing from it. It is written from the pages' statement of the methods:
 * "3.9 Optimizers", section "Lion: Learning the Sign of the Update" and its
   exercise 5: the Lion step.
 
+``train_ops`` holds the operators around the step (embedding, layer norm, 8-bit
+activation checkpoints, weight gradient) from their formulas.
+
 Every function is pinned by tests against values the pages print, closed
 forms, or library routines (see tests/test_oracle_*.py). No function is
 "parity unpinned".
