@@ -19,6 +19,9 @@ from . import _lib as L
 from .api import _DT, _dt
 
 _TOKENS = {torch.int32: 4, torch.int64: 8}
+# (not the public calls: those build objects, 0.3 to 1.7 us each of a call's 6)
+_current_device, _current_stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+_STRIDED = torch.strided
 
 
 def _check(what: str, t: torch.Tensor, dtypes, shape=None) -> torch.Tensor:
@@ -27,55 +30,58 @@ def _check(what: str, t: torch.Tensor, dtypes, shape=None) -> torch.Tensor:
         raise TypeError(f"{what}: expected a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: unsupported dtype {t.dtype} ({', '.join(str(d) for d in dtypes)})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.layout != torch.strided or not t.is_contiguous():
+    if t.layout is not _STRIDED or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
     return t
 
 
 def _rows(what: str, t: torch.Tensor) -> Tuple[int, int]:
     """(rows, cols) of a tensor normalised over its last dimension."""
-    if t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{what}: expected at least one column, got {tuple(t.shape)}")
-    cols = t.shape[-1]
-    return t.numel() // cols, cols
+    shape = t.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError(f"{what}: expected at least one column, got {tuple(shape)}")
+    return t.numel() // shape[-1], shape[-1]
 
 
-def _device(*tensors: Optional[torch.Tensor]) -> torch.device:
+def _device(*tensors: Optional[torch.Tensor]) -> int:
     """The one GPU that all tensors are on: the library takes raw device pointers."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got a tensor on {dev}")
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"every tensor must be on {dev}, got one on {t.device}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor must be on {tensors[0].device}, got one on {t.device}")
+    if index < 0:
+        raise ValueError(f"expected CUDA tensors, got a tensor on {tensors[0].device}")
+    return index
 
 
-def _launch(dev: torch.device, stream, go):
-    """``go(raw stream)`` with the tensors' device current and, where a stream is
-    given, that stream too, so that what ``go`` allocates belongs to it."""
+def _here(dev: int, stream) -> bool:
+    """Whether a call goes to the current stream of the current device."""
+    return stream is None and _current_device() == dev
+
+
+def _elsewhere(dev: int, stream, call):
+    """``call()`` with the tensors' device current and, where a stream is given,
+    that stream too, so that what it allocates belongs to it."""
     if stream is None:
-        if torch._C._cuda_getDevice() == dev.index:
-            return go(torch._C._cuda_getCurrentRawStream(dev.index))
         with torch.cuda.device(dev):
-            return go(torch._C._cuda_getCurrentRawStream(dev.index))
+            return call()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     with torch.cuda.stream(stream):   # makes its device current too
-        return go(stream.cuda_stream)
+        return call()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, dev: torch.device) -> torch.Tensor:
+def _workspace(given: Optional[torch.Tensor], need: int, beside: torch.Tensor) -> torch.Tensor:
     """The caller's workspace, or one allocated for this call."""
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if given is None else given
+    return beside.new_empty(max(need, 1), dtype=torch.uint8) if given is None else given
 
 
 def _check_workspace(given: Optional[torch.Tensor]) -> None:
@@ -102,15 +108,13 @@ def embedding_forward(table: torch.Tensor, tokens: torch.Tensor, scale: float = 
     elif dtype is not None and dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     dev = _device(table, tokens, out)
-
-    def go(s):
-        nonlocal out
-        if out is None:
-            out = torch.empty(shape, dtype=dtype or table.dtype, device=dev)
-        L.check(L.lib().ma_embedding_forward(table.data_ptr(), _dt(table), rows, cols, tokens.data_ptr(), _TOKENS[tokens.dtype],
-                                             tokens.numel(), scale, out.data_ptr(), _dt(out), s))
-        return out
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: embedding_forward(table, tokens, scale, dtype, out))
+    if out is None:
+        out = table.new_empty(shape) if dtype is None else table.new_empty(shape, dtype=dtype)
+    L.check(L.lib().ma_embedding_forward(table.data_ptr(), _dt(table), rows, cols, tokens.data_ptr(), _TOKENS[tokens.dtype],
+                                         tokens.numel(), scale, out.data_ptr(), _dt(out), _current_stream(dev)))
+    return out
 
 
 def embedding_workspace_size(rows: int, cols: int, n_tokens: int) -> int:
@@ -132,18 +136,17 @@ def embedding_backward(dout: torch.Tensor, tokens: torch.Tensor, grad: torch.Ten
     if grad.dim() != 2:
         raise ValueError(f"grad: expected [rows, cols], got {tuple(grad.shape)}")
     rows, cols = grad.shape
-    if tuple(dout.shape) != (*tokens.shape, cols):
+    if dout.shape != (*tokens.shape, cols):
         raise ValueError(f"dout: expected shape {(*tokens.shape, cols)}, got {tuple(dout.shape)}")
     _check_workspace(workspace)
     n = tokens.numel()
     dev = _device(dout, tokens, grad, workspace)
-
-    def go(s):
-        ws = _workspace(workspace, embedding_workspace_size(rows, cols, n), dev)
-        L.check(L.lib().ma_embedding_backward(dout.data_ptr(), _dt(dout), tokens.data_ptr(), _TOKENS[tokens.dtype], n, rows, cols,
-                                              scale, int(bool(accumulate)), grad.data_ptr(), ws.data_ptr(), ws.numel(), s))
-        return grad
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: embedding_backward(dout, tokens, grad, scale, accumulate, workspace))
+    ws = _workspace(workspace, embedding_workspace_size(rows, cols, n), grad)
+    L.check(L.lib().ma_embedding_backward(dout.data_ptr(), _dt(dout), tokens.data_ptr(), _TOKENS[tokens.dtype], n, rows, cols,
+                                          scale, int(bool(accumulate)), grad.data_ptr(), ws.data_ptr(), ws.numel(), _current_stream(dev)))
+    return grad
 
 
 # ---------------------------------------------------------------------------
@@ -221,14 +224,12 @@ def act_pack(x: torch.Tensor, out: Optional[ActCheckpoint] = None, stream=None) 
     if out is not None:
         _check_checkpoint("out", out, rows, cols)
     dev = _device(x, *out._tensors) if out is not None else _device(x)
-
-    def go(s):
-        nonlocal out
-        if out is None:
-            out = ActCheckpoint.empty(rows, cols, dev)
-        L.check(L.lib().ma_act_pack(x.data_ptr(), _dt(x), rows, cols, *out._pointers(), s))
-        return out
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: act_pack(x, out))
+    if out is None:
+        out = ActCheckpoint.empty(rows, cols, x.device)
+    L.check(L.lib().ma_act_pack(x.data_ptr(), _dt(x), rows, cols, *out._pointers(), _current_stream(dev)))
+    return out
 
 
 def act_unpack(checkpoint: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
@@ -245,14 +246,12 @@ def act_unpack(checkpoint: ActCheckpoint, dtype: torch.dtype = torch.bfloat16, o
     elif dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     dev = _device(*checkpoint._tensors, out)
-
-    def go(s):
-        nonlocal out
-        if out is None:
-            out = torch.empty((rows, cols), dtype=dtype, device=dev)
-        L.check(L.lib().ma_act_unpack(*checkpoint._pointers(), rows, cols, out.data_ptr(), _dt(out), s))
-        return out
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: act_unpack(checkpoint, dtype, out))
+    if out is None:
+        out = checkpoint._tensors[0].new_empty((rows, cols), dtype=dtype)
+    L.check(L.lib().ma_act_unpack(*checkpoint._pointers(), rows, cols, out.data_ptr(), _dt(out), _current_stream(dev)))
+    return out
 
 
 # ---------------------------------------------------------------------------
@@ -283,18 +282,16 @@ def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias
         _check("stats", stats, (torch.float32,), (rows, 2))
     held = () if checkpoint is None else _check_checkpoint("checkpoint", checkpoint, rows, cols)._tensors
     dev = _device(x, gain, bias, out, stats, *held)
-
-    def go(s):
-        nonlocal out, stats
-        if out is None:
-            out = torch.empty_like(x) if dtype is None or dtype == x.dtype else torch.empty(x.shape, dtype=dtype, device=dev)
-        if stats is None:
-            stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        q, sc = checkpoint._pointers() if checkpoint is not None else (None, None)
-        L.check(L.lib().ma_layernorm_forward(x.data_ptr(), _dt(x), rows, cols, _ptr(gain), _ptr(bias), eps, out.data_ptr(), _dt(out),
-                                             stats.data_ptr(), q, sc, s))
-        return out, stats
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: layernorm_forward(x, gain, bias, eps, dtype, out, stats, checkpoint))
+    if out is None:
+        out = torch.empty_like(x) if dtype is None or dtype == x.dtype else x.new_empty(x.shape, dtype=dtype)
+    if stats is None:
+        stats = x.new_empty((rows, 2), dtype=torch.float32)
+    q, sc = checkpoint._pointers() if checkpoint is not None else (None, None)
+    L.check(L.lib().ma_layernorm_forward(x.data_ptr(), _dt(x), rows, cols, _ptr(gain), _ptr(bias), eps, out.data_ptr(), _dt(out),
+                                         stats.data_ptr(), q, sc, _current_stream(dev)))
+    return out, stats
 
 
 def layernorm_workspace_size(rows: int, cols: int) -> int:
@@ -330,20 +327,17 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
         _check("dx", dx, (dx_dtype,), dy.shape)
     _check_workspace(workspace)
     dev = _device(dy, xt, *held, stats, gain, dgain, dbias, dx, workspace)
-    sums = dgain is not None or dbias is not None
-
-    def go(s):
-        nonlocal dx
-        if dx is None:
-            dx = torch.empty_like(dy if xt is None else xt)
-        q, sc = x._pointers() if held else (None, None)
-        need = layernorm_workspace_size(rows, cols) if sums else 0
-        ws = _workspace(workspace, need, dev) if need or workspace is not None else None
-        L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, q, sc, rows, cols, stats.data_ptr(),
-                                              _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
-                                              _ptr(ws), ws.numel() if ws is not None else 0, s))
-        return dx
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: layernorm_backward(dy, x, stats, gain, dgain, dbias, accumulate, dx, workspace))
+    if dx is None:
+        dx = torch.empty_like(dy if xt is None else xt)
+    q, sc = x._pointers() if held else (None, None)
+    need = layernorm_workspace_size(rows, cols) if dgain is not None or dbias is not None else 0
+    ws = _workspace(workspace, need, dy) if need or workspace is not None else None
+    L.check(L.lib().ma_layernorm_backward(dy.data_ptr(), _dt(dy), _ptr(xt), xd, q, sc, rows, cols, stats.data_ptr(),
+                                          _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
+                                          _ptr(ws), ws.numel() if ws is not None else 0, _current_stream(dev)))
+    return dx
 
 
 # ---------------------------------------------------------------------------
@@ -375,11 +369,10 @@ def act_weight_grad(dy: torch.Tensor, x: ActCheckpoint, grad: torch.Tensor, accu
     _check("grad", grad, _DT, (outs, x.cols))
     _check_workspace(workspace)
     dev = _device(dy, *x._tensors, grad, workspace)
-
-    def go(s):
-        need = act_weight_grad_workspace_size(tokens, outs, x.cols, dy.dtype)
-        ws = _workspace(workspace, need, dev) if need or workspace is not None else None
-        L.check(L.lib().ma_act_weight_grad(dy.data_ptr(), _dt(dy), *x._pointers(), tokens, outs, x.cols,
-                                           grad.data_ptr(), _dt(grad), int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0, s))
-        return grad
-    return _launch(dev, stream, go)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: act_weight_grad(dy, x, grad, accumulate, workspace))
+    need = act_weight_grad_workspace_size(tokens, outs, x.cols, dy.dtype)
+    ws = _workspace(workspace, need, grad) if need or workspace is not None else None
+    L.check(L.lib().ma_act_weight_grad(dy.data_ptr(), _dt(dy), *x._pointers(), tokens, outs, x.cols, grad.data_ptr(), _dt(grad),
+                                       int(bool(accumulate)), _ptr(ws), ws.numel() if ws is not None else 0, _current_stream(dev)))
+    return grad
