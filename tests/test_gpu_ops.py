@@ -453,17 +453,17 @@ def test_weight_grad_of_no_tokens_and_nonfinite_values():
 # ---------------------------------------------------------------------------
 # streams, graphs, and the run of them together
 # ---------------------------------------------------------------------------
-def _every(seed=80):
-    """One call of every operator on small inputs: (run, outputs)."""
-    w, t = rand((500, 264), seed), tokens("zipf", 500, 700, seed + 1).to(DEV)
+def _every(n, seed=80):
+    """One call of every operator on n tokens: (run, inputs)."""
+    w, t = rand((500, 264), seed), tokens("zipf", 500, n, seed + 1).to(DEV)
     gain, bias = 1 + rand((264,), seed + 2, F32, 0.1), rand((264,), seed + 3, F32, 0.1)
     dw = rand((136, 264), seed + 4)
     ge, gg, gb = torch.empty(500, 264, device=DEV), torch.empty(264, device=DEV), torch.empty(264, device=DEV)
-    dy = rand((700, 136), seed + 5, BF16)
+    dy = rand((n, 136), seed + 5, BF16)
 
     def run(stream=None):
         x = ma.embedding_forward(w, t, scale=3.0, dtype=BF16, stream=stream)
-        ck = ma.ActCheckpoint.empty(700, 264, DEV)
+        ck = ma.ActCheckpoint.empty(n, 264, DEV)
         y, stats = ma.layernorm_forward(x, gain, bias, checkpoint=ck, stream=stream)
         yc = ma.act_pack(y, stream=stream)
         ma.act_weight_grad(dy, yc, dw, stream=stream)
@@ -473,8 +473,13 @@ def _every(seed=80):
     return run, (w, t, dy)
 
 
-def test_another_stream_gives_the_same_bits():
-    run, _ = _every()
+# in one launch, and through the sort and the joins
+BOTH = pytest.mark.parametrize("n", [700, 1500])
+
+
+@BOTH
+def test_another_stream_gives_the_same_bits(n):
+    run, _ = _every(n)
     want = [x.clone() for x in run()]
     torch.cuda.synchronize()
     s = torch.cuda.Stream(DEV)
@@ -488,9 +493,10 @@ def test_another_stream_gives_the_same_bits():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
-def test_graph_replays_match_eager_calls():
-    run, (w, t, dy) = _every()
-    run2, (w2, t2, dy2) = _every()
+@BOTH
+def test_graph_replays_match_eager_calls(n):
+    run, (w, t, dy) = _every(n)
+    run2, (w2, t2, dy2) = _every(n)
     side = torch.cuda.Stream(DEV)
     with torch.cuda.stream(side):
         run2()
@@ -499,7 +505,7 @@ def test_graph_replays_match_eager_calls():
     with torch.cuda.graph(graph):
         out = run2()
     for i in range(4):
-        new = tokens("zipf", 500, 700, 90 + i).to(DEV)
+        new = tokens("zipf", 500, n, 90 + i).to(DEV)
         t.copy_(new)
         t2.copy_(new)
         w2.mul_(1.25)
@@ -510,8 +516,9 @@ def test_graph_replays_match_eager_calls():
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
 
 
-def test_two_streams_at_once():
-    (a, _), (b, _) = _every(80), _every(180)
+@BOTH
+def test_two_streams_at_once(n):
+    (a, _), (b, _) = _every(n, 80), _every(n, 180)
     wa, wb = [x.clone() for x in a()], [x.clone() for x in b()]
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
