@@ -531,6 +531,40 @@ def test_two_streams_at_once(n):
     assert all(torch.equal(x, y) for x, y in zip(ga, wa)) and all(torch.equal(x, y) for x, y in zip(gb, wb))
 
 
+def test_offsets_past_32_bits():
+    """Operands of more than 2^32 bytes: the last rows give what a call on them alone gives."""
+    n, cols, last = (1 << 21) + 1000, 2048, 700
+    x = torch.empty(n, cols, dtype=BF16, device=DEV)
+    x.view(torch.int16).fill_(0x3F81)                    # not quite 1
+    x[-last:] = rand((last, cols), 110, BF16)
+    ck, gain = ma.ActCheckpoint.empty(n, cols, DEV), 1 + rand((cols,), 111, F32, 0.1)
+    y, stats = ma.layernorm_forward(x, gain, checkpoint=ck)
+    small = ma.ActCheckpoint.empty(last, cols, DEV)
+    ys, ss = ma.layernorm_forward(x[-last:], gain, checkpoint=small)
+    assert torch.equal(y[-last:], ys) and torch.equal(stats[-last:], ss)
+    assert torch.equal(ck.q[-last:], small.q) and torch.equal(ck.scale[-last:], small.scale)
+    packed = ma.act_pack(x)
+    assert torch.equal(packed.q[-last:], small.q) and torch.equal(packed.scale, ck.scale)
+    assert torch.equal(ma.act_unpack(packed, out=y)[-last:], ma.act_unpack(small))
+    for held, alone in ((x, x[-last:]), (ck, small)):
+        dx = ma.layernorm_backward(x, held, stats, gain, dx=y)
+        assert torch.equal(dx[-last:], ma.layernorm_backward(x[-last:], alone, ss, gain))
+    # a weight gradient whose only nonzero dy are in the last rows
+    x[:-last] = 0
+    dw = ma.act_weight_grad(x, ma.ActCheckpoint(packed.q[:, :128].contiguous(), packed.scale[:, :1].contiguous(), 128),
+                            torch.empty(cols, 128, device=DEV))
+    want, mag = T.act_weight_grad(f64(x[-last:]), f64(ma.act_unpack(small)[:, :128]))
+    close(dw, want, 2 * (last + 16) * U * mag)
+    # a table's last rows, looked up by the last tokens
+    t = torch.full((n,), -1, device=DEV)
+    t[-last:] = n - 1 - torch.arange(last, device=DEV) // 2
+    assert torch.equal(ma.embedding_forward(x, t, out=y)[-last:], x[t[-last:]]) and not y[:-last].any()
+    del y, ck, packed
+    grad = ma.embedding_backward(x, t, torch.empty(n, cols, device=DEV))
+    pairs = x[-last:].float().view(-1, 2, cols)
+    assert torch.equal(grad[-last // 2:].flip(0), pairs[:, 0] + pairs[:, 1]) and not grad[:-last // 2].any()
+
+
 def test_training_step_end_to_end():
     """Embedding, norm with checkpoint, a linear layer, their gradients out of the checkpoints, and the optimizer
     step that reads them, against the same chain in fp64 from the stored values of each stage."""
