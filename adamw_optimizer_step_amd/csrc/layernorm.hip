@@ -10,8 +10,8 @@
 // difference of two large sums. All sums are fp32, in a fixed order. y and dx are
 // rounded once; xh is held and recomputed in fp32.
 //
-// Bound by memory: forward of 24576 x 2048 bf16 with its checkpoint, 252 MB in 48
-// to 53 us (5 TB/s); backward of 49152 x 1024 bf16, 302 MB in 52 us (5.8 TB/s) and
+// Bound by memory: forward of 24576 x 2048 bf16 with its checkpoint, 252 MB in 45
+// to 49 us (5.1 to 5.6 TB/s); backward of 49152 x 1024 bf16, 302 MB in 52 us (5.8 TB/s) and
 // 4.7 for k_norm_cols; backward out of a checkpoint of 31948 x 962 with fp32 dy,
 // 278 MB in 49 us.
 #include "rows.hpp"
@@ -52,20 +52,29 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
   __shared__ float part[2][2][1][16];
   const int t = threadIdx.x % G;
   const float per = 1.0f / (float)a.cols;
-  int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / G; row < a.rows; row += (int64_t)gridDim.x * ROWS, flip ^= 1) {
-    const unsigned char* src = elem_ptr<XD>(a.x, row * a.cols);
-    float x[CH][8];
-    {
-      Raw8<XD> raw[CH];
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
+  Raw8<XD> next[CH];
+  auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = (c * G + t) * 8;
-        raw[c] = col < a.cols ? raw_load_row<XD>(src, col, a.cols) : raw_zero<XD>();
-      }
-#pragma unroll
-      for (int c = 0; c < CH; ++c) raw_f32_row<XD>(raw[c], (c * G + t) * 8, a.cols, x[c]);
+    for (int c = 0; c < CH; ++c) {
+      const int col = (c * G + t) * 8;
+      next[c] = r < a.rows && col < a.cols ? raw_load_row<XD>(elem_ptr<XD>(a.x, r * a.cols), col, a.cols) : raw_zero<XD>();
     }
+  };
+  load(row);
+  Raw8<DT_F32> gain[CH], bias[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * G + t) * 8;
+    gain[c] = a.gain && col < a.cols ? raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols) : raw_zero<DT_F32>();
+    bias[c] = a.bias && col < a.cols ? raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.bias, 0), col, a.cols) : raw_zero<DT_F32>();
+  }
+  for (int flip = 0; row < a.rows; row += step, flip ^= 1) {
+    float x[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) raw_f32_row<XD>(next[c], (c * G + t) * 8, a.cols, x[c]);
+    if (step < a.rows) load(row + step);
     float s[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -103,12 +112,12 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = (x[c][e] - mean) * rstd;
       if (a.gain) {
-        raw_f32_row<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols), col, a.cols, w);
+        raw_f32_row<DT_F32>(gain[c], col, a.cols, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] *= w[e];
       }
       if (a.bias) {
-        raw_f32_row<DT_F32>(raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.bias, 0), col, a.cols), col, a.cols, b);
+        raw_f32_row<DT_F32>(bias[c], col, a.cols, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] += b[e];
       }
@@ -372,12 +381,18 @@ __global__ void __launch_bounds__(1024) k_norm_cols(const NormBwdArgs a) {
   }
 }
 
+// The forward pass's waves per CU: each goes through its rows with the next one's
+// loads ahead, and gain and bias in registers. Fewer wait for memory less well,
+// more spread the writes over more of it (24576 x 2048 bf16 with its checkpoint, us:
+// 49 with 16, 52 with 24, 57 with 20 or with a block per row; 4096 x 16384: 49, 58,
+// 65, 75; without the row ahead 57 and 75).
+constexpr int kNormWaves = 16;
+
 // Lanes and chunks per row by its length: f(NormShape<G, CH>).
 //
 // Forward: two chunks per lane keep twice the bytes in flight per wave and halve
-// the steps of the reductions (bf16, us: 49152 x 1024 45 against 51 with one;
-// 24576 x 2048 46 with two, 49 with one, 54 with four; 16384 x 4096 52 and 61; 8192
-// x 8192 63 and 99). Few rows leave the chip empty, and one chunk is the shorter
+// the steps of the reductions (bf16 with a checkpoint, us: 49152 x 1024 50 against 51
+// with one; 24576 x 2048 49 and 52; 8192 x 8192 62 and 77). Few rows leave the chip empty, and one chunk is the shorter
 // chain (100 rows of 1024 3.3 us against 4.0, of 4096 3.6 against 4.2, of 8192 4.3
 // against 4.6).
 //
@@ -415,7 +430,7 @@ template <int XD, int YD>
 static hipError_t norm_fwd(const NormFwdArgs& a, hipStream_t s) {
   return norm_fwd_shape(a.rows, a.cols, [&](auto sh) {
     constexpr int G = decltype(sh)::G, CH = decltype(sh)::CH;
-    const int64_t per = norm_threads(G) / G, want = (a.rows + per - 1) / per, most = (int64_t)1 << 21;
+    const int64_t per = norm_threads(G) / G, want = (a.rows + per - 1) / per, most = (int64_t)256 * kNormWaves * 64 / norm_threads(G);
     const dim3 grid((unsigned)(want < most ? want : most)), block(norm_threads(G));
     const int64_t bytes = a.rows * a.cols * (elem_bytes<XD>() + elem_bytes<YD>() + (a.q ? 1 : 0));
     if (bytes > kStreamBytes) hipLaunchKernelGGL((k_norm_fwd<XD, YD, G, CH, true>), grid, block, 0, s, a);

@@ -10,9 +10,10 @@ namespace ma {
 // cache beside anything else: they mark the larger of what they pass through as
 // non-temporal, so that it does not push out what the rest of the call, or the
 // next one, can still find there. Below it they leave the cache to the next
-// call. (Layer norm of 24576 x 2048 bf16 with its checkpoint, 252 MB: 45 us with
-// y stored non-temporally, 59 us without; of 32768 x 1024, 134 MB: 29 us both
-// ways, and a pass over y after it 22 us against 19.5.)
+// call. (Packing 24576 x 4096 bf16, 302 MB: 48 us with x loaded non-temporally, 63
+// without; layer norm of 24576 x 2048 bf16 with its checkpoint, 252 MB: 52.5 with y
+// stored so, 55 without; of 32768 x 1024, 134 MB, a pass over y after it takes 22
+// against 19.5.)
 constexpr int64_t kStreamBytes = (int64_t)192 << 20;
 
 // A 16-byte access at 2- or 4-byte alignment: gfx950 serves it as one

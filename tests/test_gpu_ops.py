@@ -179,7 +179,8 @@ def norm_inputs(rows, cols, xd, seed):
 
 NORM_SHAPES = [(1, 1), (3, 2), (5, 7), (1, 256), (9, 511), (4, 512), (6, 513), (130, 1024), (3, 1025), (2, 2048), (5, 2047), (3, 4096),
                (2, 4097), (2, 8200), (3, 16384), (2, 16383), (1000, 40), (512, 100), (513, 700), (600, 2049), (513, 1290), (1024, 300), (1025, 700), (1100, 2049),
-               (1027, 4093), (515, 8189), (1026, 8190), (2100, 130)]
+               (1027, 4093), (515, 8189), (1026, 8190), (2100, 130), (4200, 130), (4200, 530), (2100, 1100),
+               (260, 8200)]
 
 
 @pytest.mark.parametrize("rows,cols", NORM_SHAPES)
