@@ -228,7 +228,7 @@ static int act_call(const char* fn, const void* x, int32_t dtype, bool pack, int
   int rc;
   if ((rc = check_matrix(fn, rows, 0, kMaxRows, cols, kMaxCols)) || (rc = check_dtype(fn, pack ? "x" : "out", dtype))) return rc;
   const int64_t pitch = act_pitch(cols);
-  if (rows * pitch > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
+  if (rows * pitch > (dtype == MA_F32 ? kMaxElems / 2 : kMaxElems)) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements (2^35 fp32 ones)", fn);
   const Buf bufs[] = {{x, rows * cols * dt_size(dtype), (int)dt_size(dtype), !pack, false, pack ? "x" : "out"},
                       {q, rows * pitch, 16, pack, false, "q"},
                       {scale, rows * (pitch / kActBlock), 1, pack, false, "scale"}};

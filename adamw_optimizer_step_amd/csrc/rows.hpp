@@ -189,6 +189,81 @@ __device__ __forceinline__ void store_row(unsigned char* row, int col, int cols,
 }
 
 // ----------------------------------------------------------------------------
+// The same with 4 consecutive elements per lane, for fp32 streams: a wave's 16-byte
+// accesses are then one contiguous stretch, where those of 8 elements leave every
+// other 16 bytes to the next access (49152 rows of 1024 fp32 copied by index: 47 us
+// against 74, non-temporal stores included, which need whole lines).
+// ----------------------------------------------------------------------------
+template <int DT> struct Quad;
+template <> struct Quad<DT_BF16> { typedef u32x2_nt_t T __attribute__((aligned(2))); static constexpr int W = 2; };
+template <> struct Quad<DT_F32> { typedef u32x4_t T __attribute__((aligned(4))); static constexpr int W = 4; };
+template <int DT> struct Raw4 { uint32_t u[Quad<DT>::W]; };
+
+template <int DT>
+__device__ __forceinline__ Raw4<DT> quad_zero() {
+  Raw4<DT> r;
+#pragma unroll
+  for (uint32_t& u : r.u) u = 0;
+  return r;
+}
+
+// Elements col .. col+3 (col < cols) of the row; its last, partial group loads the
+// row's last 4 elements, and quad_f32 moves them to their places.
+template <int DT, bool NT = false>
+__device__ __forceinline__ Raw4<DT> quad_load_row(const unsigned char* row, int col, int cols) {
+  typedef typename Quad<DT>::T V;
+  Raw4<DT> r = quad_zero<DT>();
+  if (cols >= 4) {
+    const V* p = reinterpret_cast<const V*>(row + (int64_t)(col + 4 <= cols ? col : cols - 4) * elem_bytes<DT>());
+    V v;
+    if constexpr (NT) v = __builtin_nontemporal_load(p);
+    else v = *p;
+#pragma unroll
+    for (int i = 0; i < Quad<DT>::W; ++i) r.u[i] = v[i];
+    return r;
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (k >= cols) continue;
+    if constexpr (DT == DT_BF16) r.u[k / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k] << (16 * (k % 2));
+    else r.u[k] = reinterpret_cast<const uint32_t*>(row)[k];
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void quad_f32(const Raw4<DT>& r, int col, int cols, float (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == DT_BF16) v[i] = __uint_as_float(i & 1 ? r.u[i / 2] & 0xFFFF0000u : r.u[i / 2] << 16);
+    else v[i] = __uint_as_float(r.u[i]);
+  }
+  if ((cols & 3) == 0) return;
+  const int by = col + 4 - cols;   // elements too far up
+  if (by <= 0 || cols < 4) return;
+  if (by & 2) { v[0] = v[2]; v[1] = v[3]; v[2] = v[3] = 0.0f; }
+  if (by & 1) { v[0] = v[1]; v[1] = v[2]; v[2] = v[3]; v[3] = 0.0f; }
+}
+
+// v to elements col .. col+3 of the row (those inside it), rounded once.
+template <int DT, bool NT = false>
+__device__ __forceinline__ void quad_store_row(unsigned char* row, int col, int cols, const float (&v)[4]) {
+  typedef typename Quad<DT>::T V;
+  unsigned char* p = row + (int64_t)col * elem_bytes<DT>();
+  if (col + 4 <= cols) {
+    V u;
+    if constexpr (DT == DT_BF16) u = V{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else u = V{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    if constexpr (NT) __builtin_nontemporal_store(u, reinterpret_cast<V*>(p));
+    else *reinterpret_cast<V*>(p) = u;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < cols) store1<DT>(p, i, v[i]);
+}
+
+// ----------------------------------------------------------------------------
 // The 8-bit checkpoint: per row and block of 128 columns, one power of two
 // 2^e and e4m3 values q = RNE(x / 2^e). e is the least exponent with
 // amax <= 448 * 2^e, kept in [kActEmin, kActEmax]; the stored byte is e + 127.
@@ -214,16 +289,24 @@ __device__ __forceinline__ int act_exponent(float amax) {
 
 __device__ __forceinline__ float act_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// The exponent of the block that the 16 lanes 16j .. 16j+15 hold, 8 columns
-// each. Magnitudes are compared as their bits, where infinities and NaN stand
+// The exponent of the block that the 16 lanes 16j .. 16j+15 hold, E = 8 columns
+// each, or the 32 lanes 32j .. 32j+31 with E = 4. Magnitudes are compared as their bits, where infinities and NaN stand
 // above every finite value: a block without any is done in one pass, another
 // goes over its values again without them.
-__device__ __forceinline__ int act_block_exponent(const float (&v)[8]) {
+template <int E>
+__device__ __forceinline__ int act_block_exponent(const float (&v)[E]) {
   constexpr uint32_t kInf = 0x7F800000u;
-  auto over = [](uint32_t a) __attribute__((always_inline)) { return reduce16(a, [](uint32_t x, uint32_t y) { return x > y ? x : y; }); };
+  auto over = [](uint32_t a) __attribute__((always_inline)) {
+    a = reduce16(a, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+    if constexpr (E == 4) {
+      const uint32_t b = (uint32_t)__shfl_xor((int)a, 16, 64);
+      a = a > b ? a : b;
+    }
+    return a;
+  };
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < E; ++i) {
     const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
     a = a > m ? a : m;
   }
@@ -231,7 +314,7 @@ __device__ __forceinline__ int act_block_exponent(const float (&v)[8]) {
   if (__any(a >= kInf)) {
     a = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < E; ++i) {
       const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
       a = m < kInf && m > a ? m : a;
     }
@@ -240,35 +323,46 @@ __device__ __forceinline__ int act_block_exponent(const float (&v)[8]) {
   return act_exponent(__uint_as_float(a));
 }
 
-// 8 values over 2^e as e4m3 bytes. Every finite value is within 448 * 2^e but
+// 8 (or 4) values over 2^e as e4m3 bytes. Every finite value is within 448 * 2^e but
 // for those of the largest exponent; NaN and what exceeds the range, here the
 // infinities, become NaN.
-__device__ __forceinline__ uint2 act_encode(const float (&v)[8], int e) {
+template <int E>
+__device__ __forceinline__ void act_encode(const float (&v)[E], int e, uint32_t (&q)[E / 4]) {
   const float inv = act_pow2(-e);
-  float t[8];
+  float t[E];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
+  for (int i = 0; i < E; ++i) t[i] = v[i] * inv;
   if (e == kActEmax) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < E; ++i)
       if (__builtin_fabsf(t[i]) < __builtin_inff()) t[i] = __builtin_fminf(__builtin_fmaxf(t[i], -240.0f), 240.0f);
   }
-  uint32_t lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], hi, true);
-  return make_uint2(lo, hi);
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    uint32_t b = 0;
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * i], t[4 * i + 1], b, false);
+    q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * i + 2], t[4 * i + 3], b, true);
+  }
+}
+__device__ __forceinline__ uint2 act_encode(const float (&v)[8], int e) {
+  uint32_t q[2];
+  act_encode<8>(v, e, q);
+  return make_uint2(q[0], q[1]);
 }
 
 __device__ __forceinline__ float act_scale(uint32_t b) { return __uint_as_float(b << 23); }
 
-// 8 e4m3 bytes times s (a power of two)
-__device__ __forceinline__ void act_decode(uint2 q, float s, float (&v)[8]) {
-  const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.x, s, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.x, s, true);
-  const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.y, s, false), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.y, s, true);
+// 4 or 8 e4m3 bytes times s (a power of two)
+__device__ __forceinline__ void act_decode(uint32_t q, float s, float (&v)[4]) {
+  const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, s, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q, s, true);
   v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
-  v[4] = c[0]; v[5] = c[1]; v[6] = d[0]; v[7] = d[1];
+}
+__device__ __forceinline__ void act_decode(uint2 q, float s, float (&v)[8]) {
+  float a[4], b[4];
+  act_decode(q.x, s, a);
+  act_decode(q.y, s, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
 }
 
 // 4 e4m3 bytes times s as packed bf16, exact

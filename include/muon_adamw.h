@@ -406,7 +406,7 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
  * NaN. Every held value is exact in bf16: unpacking rounds nothing, and the
  * error against x is at most 2^-4 |x|, or 2^-10 * 2^e for values below the
  * block's e4m3 normal range (2^-6 * 2^e). Limits: rows, cols <= 2^24, rows * P
- * <= 2^36. */
+ * <= 2^36 (2^35 where x or out is fp32). */
 #define MA_ACT_BLOCK 128
 int ma_act_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, uint8_t* q, uint8_t* scale, void* stream);
 int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, void* out, int32_t out_dtype,

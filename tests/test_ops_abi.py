@@ -73,7 +73,7 @@ BAD = [
     ("ma_layernorm_backward", dict(x=None, ckpt_q=at(8), ckpt_scale=at(9), dy_dtype=0, dx_dtype=1), UNS),
     ("ma_act_pack", dict(x=None), INV), ("ma_act_pack", dict(q=at(1) + 4), INV), ("ma_act_pack", dict(q=at(0)), INV),
     ("ma_act_pack", dict(x_dtype=2), UNS), ("ma_act_pack", dict(cols=0), INV), ("ma_act_pack", dict(scale=None), INV),
-    ("ma_act_pack", dict(rows=1 << 24, cols=(1 << 14) + 1), INV),
+    ("ma_act_pack", dict(rows=1 << 24, cols=(1 << 14) + 1), INV), ("ma_act_pack", dict(rows=1 << 24, cols=(1 << 11) + 1, x_dtype=0), INV),
     ("ma_act_unpack", dict(out=at(0)), INV), ("ma_act_unpack", dict(out_dtype=4), UNS), ("ma_act_unpack", dict(out=at(2) + 1), INV),
     ("ma_act_unpack", dict(q=None), INV),
     ("ma_act_weight_grad", dict(dy=None), INV), ("ma_act_weight_grad", dict(q=None), INV), ("ma_act_weight_grad", dict(scale=None), INV),
