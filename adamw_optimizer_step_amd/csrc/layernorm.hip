@@ -46,57 +46,92 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*part)[16]) {
   }
 }
 
+// Chunk c of a row: the G lanes' 8 values each of G * 8 columns, 8 consecutive ones
+// per lane, or two times 4 where an operand is fp32 (rows.hpp, quad_load_row).
+template <int DT, int G, bool QUADS> struct Chunk {
+  Raw8<DT> r = raw_zero<DT>();
+  static constexpr int H = 1, E = 8;   // parts of E values
+  static __device__ __forceinline__ int col(int c, int, int t) { return (c * G + t) * 8; }
+  __device__ __forceinline__ void load(const unsigned char* row, int c, int t, int cols) {
+    if (col(c, 0, t) < cols) r = raw_load_row<DT>(row, col(c, 0, t), cols);
+  }
+  __device__ __forceinline__ void f32(int c, int, int t, int cols, float (&v)[8]) const { raw_f32_row<DT>(r, col(c, 0, t), cols, v); }
+  template <bool NT> static __device__ __forceinline__ void store(unsigned char* row, int col, int cols, const float (&v)[8]) { store_row<DT, NT>(row, col, cols, v); }
+};
+template <int DT, int G> struct Chunk<DT, G, true> {
+  Raw4<DT> r[2] = {quad_zero<DT>(), quad_zero<DT>()};
+  static constexpr int H = 2, E = 4;
+  static __device__ __forceinline__ int col(int c, int h, int t) { return (c * 2 + h) * G * 4 + t * 4; }
+  __device__ __forceinline__ void load(const unsigned char* row, int c, int t, int cols) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (col(c, h, t) < cols) r[h] = quad_load_row<DT>(row, col(c, h, t), cols);
+  }
+  __device__ __forceinline__ void f32(int c, int h, int t, int cols, float (&v)[4]) const { quad_f32<DT>(r[h], col(c, h, t), cols, v); }
+  template <bool NT> static __device__ __forceinline__ void store(unsigned char* row, int col, int cols, const float (&v)[4]) { quad_store_row<DT, NT>(row, col, cols, v); }
+};
+
 template <int XD, int YD, int G, int CH, bool NT>
 __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs a) {
   constexpr int ROWS = norm_threads(G) / G;
+  constexpr bool QUADS = XD == DT_F32 || YD == DT_F32;
+  typedef Chunk<XD, G, QUADS> XC;
+  typedef Chunk<DT_F32, G, QUADS> PC;
+  constexpr int H = XC::H, E = XC::E;
   __shared__ float part[2][2][1][16];
   const int t = threadIdx.x % G;
   const float per = 1.0f / (float)a.cols;
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / G;
-  Raw8<XD> next[CH];
+  XC next[CH];
   auto load = [&](int64_t r) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * G + t) * 8;
-      next[c] = r < a.rows && col < a.cols ? raw_load_row<XD>(elem_ptr<XD>(a.x, r * a.cols), col, a.cols) : raw_zero<XD>();
+      next[c] = XC();
+      if (r < a.rows) next[c].load(elem_ptr<XD>(a.x, r * a.cols), c, t, a.cols);
     }
   };
   load(row);
-  Raw8<DT_F32> gain[CH], bias[CH];
+  PC gain[CH], bias[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int col = (c * G + t) * 8;
-    gain[c] = a.gain && col < a.cols ? raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.gain, 0), col, a.cols) : raw_zero<DT_F32>();
-    bias[c] = a.bias && col < a.cols ? raw_load_row<DT_F32>(elem_ptr<DT_F32>(a.bias, 0), col, a.cols) : raw_zero<DT_F32>();
+    if (a.gain) gain[c].load(elem_ptr<DT_F32>(a.gain, 0), c, t, a.cols);
+    if (a.bias) bias[c].load(elem_ptr<DT_F32>(a.bias, 0), c, t, a.cols);
   }
   for (int flip = 0; row < a.rows; row += step, flip ^= 1) {
-    float x[CH][8];
+    float x[CH][H][E];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) raw_f32_row<XD>(next[c], (c * G + t) * 8, a.cols, x[c]);
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int h = 0; h < H; ++h) next[c].f32(c, h, t, a.cols, x[c][h]);
     if (step < a.rows) load(row + step);
     float s[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += x[c][e];
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[0] += x[c][h][e];
     group_sum<G>(s, part[flip][0]);
     const float mean = s[0] * per;
     float q[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int in = a.cols - (c * G + t) * 8;
-      if (in >= 8) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = x[c][e] - mean;
-          q[0] = __builtin_fmaf(d, d, q[0]);
-        }
-      } else if (in > 0) {
+      for (int h = 0; h < H; ++h) {
+        const int in = a.cols - XC::col(c, h, t);
+        if (in >= E) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = e < in ? x[c][e] - mean : 0.0f;
-          q[0] = __builtin_fmaf(d, d, q[0]);
+          for (int e = 0; e < E; ++e) {
+            const float d = x[c][h][e] - mean;
+            q[0] = __builtin_fmaf(d, d, q[0]);
+          }
+        } else if (in > 0) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float d = e < in ? x[c][h][e] - mean : 0.0f;
+            q[0] = __builtin_fmaf(d, d, q[0]);
+          }
         }
       }
     }
@@ -106,32 +141,42 @@ __global__ void __launch_bounds__(norm_threads(G)) k_norm_fwd(const NormFwdArgs 
     unsigned char* dst = elem_ptr<YD>(a.y, row * a.cols);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * G + t) * 8;
-      if (col >= a.cols) continue;
-      float y[8], w[8], b[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = (x[c][e] - mean) * rstd;
-      if (a.gain) {
-        raw_f32_row<DT_F32>(gain[c], col, a.cols, w);
+      for (int h = 0; h < H; ++h) {
+        const int col = XC::col(c, h, t);
+        if (col >= a.cols) continue;
+        float y[E], w[E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= w[e];
+        for (int e = 0; e < E; ++e) y[e] = (x[c][h][e] - mean) * rstd;
+        if (a.gain) {
+          gain[c].f32(c, h, t, a.cols, w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] *= w[e];
+        }
+        if (a.bias) {
+          bias[c].f32(c, h, t, a.cols, w);
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] += w[e];
+        }
+        Chunk<YD, G, QUADS>::template store<NT>(dst, col, a.cols, y);
       }
-      if (a.bias) {
-        raw_f32_row<DT_F32>(bias[c], col, a.cols, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += b[e];
-      }
-      store_row<YD, NT>(dst, col, a.cols, y);
     }
     if (a.q) {
       const int64_t pitch = act_pitch(a.cols);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int col = (c * G + t) * 8;
-        const int e = act_block_exponent(x[c]);
-        if (col >= pitch) continue;
-        *reinterpret_cast<uint2*>(a.q + row * pitch + col) = act_encode(x[c], e);
-        if (t % 16 == 0) a.qscale[row * (pitch / kActBlock) + col / kActBlock] = (uint8_t)(e + 127);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const int col = XC::col(c, h, t);
+          const int e = act_block_exponent(x[c][h]);
+          if (col >= pitch) continue;
+          uint32_t b[E / 4];
+          act_encode<E>(x[c][h], e, b);
+          uint8_t* to = a.q + row * pitch + col;
+          if constexpr (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(b[0], b[1]);
+          else *reinterpret_cast<uint32_t*>(to) = b[0];
+          if (t % (kActBlock / E) == 0) a.qscale[row * (pitch / kActBlock) + col / kActBlock] = (uint8_t)(e + 127);
+        }
       }
     }
   }
