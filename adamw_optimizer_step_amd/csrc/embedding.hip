@@ -273,65 +273,87 @@ __global__ void __launch_bounds__(kBinThreads) k_embed_bin(const EmbedBwdArgs a)
 // that its first position belongs to goes to partial row 2p, that of another
 // long run that its last position belongs to to 2p + 1 (no third one fits), and
 // k_embed_join adds a run's parts in order.
-// 49152 tokens x 1024 bf16 into 50304 rows: 65 us (100 MB read, 206 written, 49 at
-// the rate of a large copy); 70 with two rows per wave, 79 with four.
+// 49152 tokens x 1024 bf16 into 50304 rows: 53 us (100 MB read, 206 written, 49 at
+// the rate of a large copy); 65 with 8 columns per lane, their place checked at each
+// load and cached stores; two rows per wave 70, four 79.
 // ---------------------------------------------------------------------------
+// A lane's columns of a slice: 4 from col + 256 k, k < 2 CH (see quad_load_row). Every
+// lane loads 4 columns inside the row, so that the loads are free of branches: the
+// row's last, partial group its last 4, moved to their places once the sum is
+// whole; lanes past the row's end anything, which is not stored.
 template <int DD, int CH>
-__device__ __forceinline__ void embed_sum(const EmbedBwdArgs& a, int32_t pos, int from, int to, int col, float (&acc)[CH][8]) {
+__device__ __forceinline__ void embed_sum(const EmbedBwdArgs& a, int32_t pos, int from, int to, int col, float (&acc)[2 * CH][4]) {
+  constexpr int Q = 2 * CH;
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
+  for (int k = 0; k < Q; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[c][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) acc[k][e] = 0.0f;
+  if (__builtin_expect(a.cols < 4, 0)) {
+#pragma unroll 1
+    for (int j = from; j < to; ++j) {
+      float v[4];
+      quad_f32<DD>(quad_load_row<DD>(elem_ptr<DD>(a.dout, (int64_t)__builtin_amdgcn_readlane(pos, j) * a.cols), 0, a.cols), 0, a.cols, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][e] += v[e];
+    }
+    return;
+  }
+  int at[Q];
+#pragma unroll
+  for (int k = 0; k < Q; ++k) at[k] = (col + k * 256 + 4 <= a.cols ? col + k * 256 : a.cols - 4) * elem_bytes<DD>();
+  typedef typename Quad<DD>::T V;
   constexpr int U = (DD == DT_BF16 ? 16 : 8) / CH;   // 64 registers of rows in flight; each row is read once (non-temporal)
   for (int j = from; j < to; j += U) {
-    Raw8<DD> x[U][CH];
+    Raw4<DD> x[U][Q];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (j + u < to) {
-        const int64_t p = __builtin_amdgcn_readlane(pos, j + u);
-        const unsigned char* row = elem_ptr<DD>(a.dout, p * a.cols);
+        const unsigned char* row = elem_ptr<DD>(a.dout, (int64_t)__builtin_amdgcn_readlane(pos, j + u) * a.cols);
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-          x[u][c] = col + c * 512 < a.cols ? raw_load_row<DD, true>(row, col + c * 512, a.cols) : raw_zero<DD>();
+        for (int k = 0; k < Q; ++k) x[u][k].u = __builtin_nontemporal_load(reinterpret_cast<const V*>(row + at[k]));
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (j + u < to) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          float v[8];
-          raw_f32_row<DD>(x[u][c], col + c * 512, a.cols, v);
+        for (int k = 0; k < Q; ++k) {
+          float v[4];
+          quad_f32<DD>(x[u][k], 0, 0, v);   // (as they are)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[c][e] += v[e];
+          for (int e = 0; e < 4; ++e) acc[k][e] += v[e];
         }
       }
     }
   }
-}
-
-// A row's sum, scaled, to the gradient, or added to what is there.
-template <int CH, bool ACC>
-__device__ __forceinline__ void embed_store(const EmbedBwdArgs& a, int64_t v, int col, float (&acc)[CH][8]) {
-  unsigned char* out = reinterpret_cast<unsigned char*>(a.grad + v * a.cols);
+  if (a.cols & 3) {
 #pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    const int cc = col + k * 512;
-    if (cc >= a.cols) continue;
-    float old[8] = {};
-    if constexpr (ACC) raw_f32_row<DT_F32>(raw_load_row<DT_F32>(out, cc, a.cols), cc, a.cols, old);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[k][e] = ACC ? __fadd_rn(old[e], __fmul_rn(acc[k][e], a.scale)) : acc[k][e] * a.scale;
-    store_row<DT_F32>(out, cc, a.cols, acc[k]);
+    for (int k = 0; k < Q; ++k) quad_fix(col + k * 256, a.cols, acc[k]);
   }
 }
 
-template <int DD, int CH, bool ACC>
+// A row's sum, scaled, to the gradient, or added to what is there.
+template <int CH, bool ACC, bool NT = false>
+__device__ __forceinline__ void embed_store(const EmbedBwdArgs& a, int64_t v, int col, float (&acc)[2 * CH][4]) {
+  unsigned char* out = reinterpret_cast<unsigned char*>(a.grad + v * a.cols);
+#pragma unroll
+  for (int k = 0; k < 2 * CH; ++k) {
+    const int cc = col + k * 256;
+    if (cc >= a.cols) continue;
+    float old[4] = {};
+    if constexpr (ACC) quad_f32<DT_F32>(quad_load_row<DT_F32>(out, cc, a.cols), cc, a.cols, old);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[k][e] = ACC ? __fadd_rn(old[e], __fmul_rn(acc[k][e], a.scale)) : acc[k][e] * a.scale;
+    quad_store_row<DT_F32, NT>(out, cc, a.cols, acc[k]);
+  }
+}
+
+template <int DD, int CH, bool ACC, bool NT>
 __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int piece_blocks) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = blockIdx.y * 512 * CH + lane * 8;
-  float acc[CH][8];
+  const int col = blockIdx.y * 512 * CH + lane * 4;
+  float acc[2 * CH][4];
   if ((int)blockIdx.x < piece_blocks) {
     const int64_t p = (int64_t)blockIdx.x * 4 + wave;
     const int64_t first = p * a.piece;
@@ -350,8 +372,8 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int pie
       embed_sum<DD, CH>(a, pos, from, to, col, acc);
       unsigned char* out = reinterpret_cast<unsigned char*>(a.partial + (2 * p + side) * a.cols);
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
-        if (col + k * 512 < a.cols) store_row<DT_F32>(out, col + k * 512, a.cols, acc[k]);
+      for (int k = 0; k < 2 * CH; ++k)
+        if (col + k * 256 < a.cols) quad_store_row<DT_F32>(out, col + k * 256, a.cols, acc[k]);
     }
     return;
   }
@@ -364,7 +386,7 @@ __global__ void __launch_bounds__(256) k_embed_sum(const EmbedBwdArgs a, int pie
   const int64_t s = a.start[slot];
   const int32_t pos = lane < c ? a.order[s + lane] : 0;
   embed_sum<DD, CH>(a, pos, 0, c, col, acc);
-  embed_store<CH, ACC>(a, v, col, acc);
+  embed_store<CH, ACC, NT>(a, v, col, acc);
 }
 
 // The long runs that start in one of the block's kJoinPieces pieces (at most one
@@ -443,22 +465,22 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_embed_join(const EmbedBwdAr
 // shared out among the block's waves and joined in order (500 tokens into 1000 x
 // 1024, the most frequent 67 times: 16 -> 10.5 us; 500 equal ones: 164 -> 50). When the gradient is
 // written whole, the other blocks write zeros to the rows that no token names,
-// kDirectRows each, flagged in LDS: few, as a short front of writes moves over
-// memory fastest (zeros of 206 MB in order: 6.5 TB/s by blocks of 4 KB, 5.5 of 64
-// KB), but each block reads all tokens (500 into 50304 x 1024: 38.5 us with 16 rows,
-// 40.4 with 64, 37.7 with 4, where 30000 x 64 goes from 7.7 to 11.4).
+// flagged in LDS, 16 rows a block or up to kDirectRows short ones: few, as a short
+// front of writes moves over memory fastest (zeros of 206 MB in order: 6.5 TB/s by
+// blocks of 4 KB, 5.5 of 64 KB), but each block reads all tokens (500 into 50304 x
+// 1024: 38.5 us with 16 rows, 40.4 with 64; into 60000 x 64 11.8 and 9.9).
 // ---------------------------------------------------------------------------
-constexpr int kDirectWaves = 8, kDirectAlone = 16, kDirectRows = 16, kDirectWords = kEmbedDirect / 64;
+constexpr int kDirectWaves = 8, kDirectAlone = 16, kDirectRows = 64, kDirectWords = kEmbedDirect / 64;
 
 template <int DD, int CH, bool ACC, bool WIDE>
-__global__ void __launch_bounds__(kDirectWaves * 64) k_embed_direct(const EmbedBwdArgs a, int token_blocks) {
+__global__ void __launch_bounds__(kDirectWaves * 64) k_embed_direct(const EmbedBwdArgs a, int token_blocks, int fill_rows) {
   __shared__ uint16_t found[kDirectWaves][kEmbedDirect];
   __shared__ float part[kDirectWaves][CH * 8][64];
   __shared__ uint32_t counts[kDirectWaves];
   __shared__ uint32_t named[kDirectRows];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = blockIdx.y * 512 * CH + lane * 8;
+  const int col = blockIdx.y * 512 * CH + lane * 4;
   const int n = (int)a.n_tokens;
   if ((int)blockIdx.x < token_blocks) {
     uint32_t t[kDirectWords];
@@ -484,7 +506,7 @@ __global__ void __launch_bounds__(kDirectWaves * 64) k_embed_direct(const EmbedB
       }
     }
     if (lane == 0) counts[wave] = count > kDirectAlone ? count : 0;
-    float acc[CH][8];
+    float acc[2 * CH][4];
     if (count > 0 && count <= kDirectAlone) {
       embed_sum<DD, CH>(a, lane < count ? found[wave][lane] : 0, 0, count, col, acc);
       embed_store<CH, ACC>(a, v, col, acc);
@@ -499,44 +521,45 @@ __global__ void __launch_bounds__(kDirectWaves * 64) k_embed_direct(const EmbedB
         const int some = left - i < 64 ? left - i : 64;
         embed_sum<DD, CH>(a, lane < some ? found[owner][from + i + lane] : 0, 0, some, col, acc);
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
+        for (int k = 0; k < 2 * CH; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* const p = &part[wave][k * 8 + e][lane];
+          for (int e = 0; e < 4; ++e) {
+            float* const p = &part[wave][k * 4 + e][lane];
             *p = i ? *p + acc[k][e] : acc[k][e];
           }
       }
       __syncthreads();
       if (wave == owner) {
+#pragma unroll 1
+        for (int w = 0; w < kDirectWaves; ++w) {
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
+          for (int k = 0; k < 2 * CH; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float s = part[0][k * 8 + e][lane];
-#pragma unroll
-            for (int w = 1; w < kDirectWaves; ++w) s += part[w][k * 8 + e][lane];
-            acc[k][e] = s;
-          }
+            for (int e = 0; e < 4; ++e) {
+              const float x = part[w][k * 4 + e][lane];
+              acc[k][e] = w ? acc[k][e] + x : x;
+            }
+        }
         embed_store<CH, ACC>(a, v, col, acc);
       }
       __syncthreads();
     }
     return;
   }
-  const int64_t first = (int64_t)((int)blockIdx.x - token_blocks) * kDirectRows;
-  if (threadIdx.x < kDirectRows) named[threadIdx.x] = 0;
+  const int64_t first = (int64_t)((int)blockIdx.x - token_blocks) * fill_rows;
+  if ((int)threadIdx.x < fill_rows) named[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kEmbedDirect; i += kDirectWaves * 64) {
     if (i + (int)threadIdx.x < n) {
       const int64_t v = token_at(a.tokens, WIDE, i + threadIdx.x) - first;
-      if (v >= 0 && v < kDirectRows) named[v] = 1;   // (every writer writes the same)
+      if (v >= 0 && v < fill_rows) named[v] = 1;   // (every writer writes the same)
     }
   }
   __syncthreads();
   typedef typename U16<DT_F32>::T V;
   const int c0 = blockIdx.y * 512 * CH, c1 = a.cols < c0 + 512 * CH ? a.cols : c0 + 512 * CH;
-  for (int r = wave; r < kDirectRows && first + r < a.rows; r += kDirectWaves) {
+  for (int r = wave; r < fill_rows && first + r < a.rows; r += kDirectWaves) {
     if (named[r]) continue;
     float* out = a.grad + (first + r) * a.cols;
     for (int c = c0 + lane * 4; c < c1; c += 256) {
@@ -583,9 +606,10 @@ template <int DD, int CH>
 static void embed_sum_launch(const EmbedBwdArgs& a, hipStream_t s) {
   if (a.n_tokens <= kEmbedDirect) {
     const int tb = (int)((a.n_tokens + kDirectWaves - 1) / kDirectWaves);
-    const int64_t fill = a.accumulate ? 0 : (a.rows + kDirectRows - 1) / kDirectRows;
+    const int fr = a.cols <= 256 ? kDirectRows : (a.cols <= 512 ? kDirectRows / 2 : kDirectRows / 4);
+    const int64_t fill = a.accumulate ? 0 : (a.rows + fr - 1) / fr;
     const dim3 grid((unsigned)(tb + fill), (unsigned)((a.cols + 512 * CH - 1) / (512 * CH)));
-    auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(kDirectWaves * 64), 0, s, a, tb); };
+    auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(kDirectWaves * 64), 0, s, a, tb, fr); };
     if (a.accumulate) a.wide ? go(k_embed_direct<DD, CH, true, true>) : go(k_embed_direct<DD, CH, true, false>);
     else a.wide ? go(k_embed_direct<DD, CH, false, true>) : go(k_embed_direct<DD, CH, false, false>);
     return;
@@ -593,8 +617,9 @@ static void embed_sum_launch(const EmbedBwdArgs& a, hipStream_t s) {
   const int64_t pieces = embed_pieces(a.n_tokens);
   const int pb = (int)((pieces + 3) / 4);
   const dim3 grid((unsigned)(pb + (a.rows + 3) / 4), (unsigned)((a.cols + 512 * CH - 1) / (512 * CH)));
-  if (a.accumulate) hipLaunchKernelGGL((k_embed_sum<DD, CH, true>), grid, dim3(256), 0, s, a, pb);
-  else hipLaunchKernelGGL((k_embed_sum<DD, CH, false>), grid, dim3(256), 0, s, a, pb);
+  if (a.accumulate) hipLaunchKernelGGL((k_embed_sum<DD, CH, true, false>), grid, dim3(256), 0, s, a, pb);
+  else if (a.rows * a.cols * 4 > kStreamBytes) hipLaunchKernelGGL((k_embed_sum<DD, CH, false, true>), grid, dim3(256), 0, s, a, pb);
+  else hipLaunchKernelGGL((k_embed_sum<DD, CH, false, false>), grid, dim3(256), 0, s, a, pb);
 }
 
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dout_dt, hipStream_t s) {

@@ -195,40 +195,53 @@ __device__ __forceinline__ void store_row(unsigned char* row, int col, int cols,
 // against 74, non-temporal stores included, which need whole lines).
 // ----------------------------------------------------------------------------
 template <int DT> struct Quad;
-template <> struct Quad<DT_BF16> { typedef u32x2_nt_t T __attribute__((aligned(2))); static constexpr int W = 2; };
-template <> struct Quad<DT_F32> { typedef u32x4_t T __attribute__((aligned(4))); static constexpr int W = 4; };
-template <int DT> struct Raw4 { uint32_t u[Quad<DT>::W]; };
+template <> struct Quad<DT_BF16> { typedef u32x2_nt_t R; typedef u32x2_nt_t T __attribute__((aligned(2))); };
+template <> struct Quad<DT_F32> { typedef u32x4_t R; typedef u32x4_t T __attribute__((aligned(4))); };
+template <int DT> struct Raw4 { typename Quad<DT>::R u; };
 
 template <int DT>
 __device__ __forceinline__ Raw4<DT> quad_zero() {
   Raw4<DT> r;
-#pragma unroll
-  for (uint32_t& u : r.u) u = 0;
+  r.u = (typename Quad<DT>::R)(0u);
   return r;
 }
 
 // Elements col .. col+3 (col < cols) of the row; its last, partial group loads the
-// row's last 4 elements, and quad_f32 moves them to their places.
+// row's last 4 elements, and quad_f32 moves them to their places. Rows of fewer
+// than 4 elements are put together one by one.
 template <int DT, bool NT = false>
 __device__ __forceinline__ Raw4<DT> quad_load_row(const unsigned char* row, int col, int cols) {
   typedef typename Quad<DT>::T V;
-  Raw4<DT> r = quad_zero<DT>();
+  Raw4<DT> r;
   if (cols >= 4) {
     const V* p = reinterpret_cast<const V*>(row + (int64_t)(col + 4 <= cols ? col : cols - 4) * elem_bytes<DT>());
-    V v;
-    if constexpr (NT) v = __builtin_nontemporal_load(p);
-    else v = *p;
-#pragma unroll
-    for (int i = 0; i < Quad<DT>::W; ++i) r.u[i] = v[i];
+    if constexpr (NT) r.u = __builtin_nontemporal_load(p);
+    else r.u = *p;
     return r;
   }
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (k >= cols) continue;
-    if constexpr (DT == DT_BF16) r.u[k / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k] << (16 * (k % 2));
-    else r.u[k] = reinterpret_cast<const uint32_t*>(row)[k];
+  r = quad_zero<DT>();
+#pragma unroll 1
+  for (int k = cols - 1; k >= 0; --k) {
+    if constexpr (DT == DT_BF16) {
+      r.u[1] = r.u[1] << 16 | r.u[0] >> 16;
+      r.u[0] = r.u[0] << 16 | reinterpret_cast<const uint16_t*>(row)[k];
+    } else {
+      r.u[3] = r.u[2];
+      r.u[2] = r.u[1];
+      r.u[1] = r.u[0];
+      r.u[0] = reinterpret_cast<const uint32_t*>(row)[k];
+    }
   }
   return r;
+}
+
+// The values that quad_load_row(row, col, cols) read, with every one in its place
+// and zeros past the row's end.
+__device__ __forceinline__ void quad_fix(int col, int cols, float (&v)[4]) {
+  const int by = col + 4 - cols;   // elements too far up
+  if (by <= 0 || cols < 4) return;
+  if (by & 2) { v[0] = v[2]; v[1] = v[3]; v[2] = v[3] = 0.0f; }
+  if (by & 1) { v[0] = v[1]; v[1] = v[2]; v[2] = v[3]; v[3] = 0.0f; }
 }
 
 template <int DT>
@@ -238,11 +251,7 @@ __device__ __forceinline__ void quad_f32(const Raw4<DT>& r, int col, int cols, f
     if constexpr (DT == DT_BF16) v[i] = __uint_as_float(i & 1 ? r.u[i / 2] & 0xFFFF0000u : r.u[i / 2] << 16);
     else v[i] = __uint_as_float(r.u[i]);
   }
-  if ((cols & 3) == 0) return;
-  const int by = col + 4 - cols;   // elements too far up
-  if (by <= 0 || cols < 4) return;
-  if (by & 2) { v[0] = v[2]; v[1] = v[3]; v[2] = v[3] = 0.0f; }
-  if (by & 1) { v[0] = v[1]; v[1] = v[2]; v[2] = v[3]; v[3] = 0.0f; }
+  if (cols & 3) quad_fix(col, cols, v);
 }
 
 // v to elements col .. col+3 of the row (those inside it), rounded once.
