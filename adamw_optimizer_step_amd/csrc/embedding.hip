@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kBinThreads) k_embed_bin(const EmbedBwdArgs a)
 // that its first position belongs to goes to partial row 2p, that of another
 // long run that its last position belongs to to 2p + 1 (no third one fits), and
 // k_embed_join adds a run's parts in order.
-// 49152 tokens x 1024 bf16 into 50304 rows: 53 us (100 MB read, 206 written, 49 at
+// 49152 tokens x 1024 bf16 into 50304 rows: 55 us (100 MB read, 206 written, 49 at
 // the rate of a large copy); 65 with 8 columns per lane, their place checked at each
 // load and cached stores; two rows per wave 70, four 79.
 // ---------------------------------------------------------------------------

@@ -10,8 +10,8 @@
 // difference of two large sums. All sums are fp32, in a fixed order. y and dx are
 // rounded once; xh is held and recomputed in fp32.
 //
-// Bound by memory: forward of 24576 x 2048 bf16 with its checkpoint, 252 MB in 45
-// to 49 us (5.1 to 5.6 TB/s); backward of 49152 x 1024 bf16, 302 MB in 52 us (5.8 TB/s) and
+// Bound by memory: forward of 24576 x 2048 bf16 with its checkpoint, 252 MB in 43
+// us (5.9 TB/s), 49 where its operands are cold; backward of 49152 x 1024 bf16, 302 MB in 52 us (5.8 TB/s) and
 // 4.7 for k_norm_cols; backward out of a checkpoint of 31948 x 962 with fp32 dy,
 // 278 MB in 49 us.
 #include "rows.hpp"
