@@ -566,6 +566,34 @@ def test_offsets_past_32_bits():
     assert torch.equal(grad[-last // 2:].flip(0), pairs[:, 0] + pairs[:, 1]) and not grad[:-last // 2].any()
 
 
+@pytest.mark.parametrize("cols", [1023, 1025, 1026])
+def test_large_calls_with_ragged_rows(cols):
+    """Calls that pass the caches (more than 192 MB) give what calls on some of their rows give."""
+    n, pick = 60000, torch.tensor([0, 1, 777, 31000, 59998, 59999], device=DEV)
+    for dt in (F32, BF16):
+        buf, x = view(rand((n, cols), 120, dt), 1)
+        for od in (F32, BF16):
+            ob, y = view(torch.zeros(n, cols, dtype=od, device=DEV), 1)
+            ck, few = ma.ActCheckpoint.empty(n, cols, DEV), ma.ActCheckpoint.empty(6, cols, DEV)
+            _, stats = ma.layernorm_forward(x, out=y, checkpoint=ck)
+            ys, ss = ma.layernorm_forward(x[pick].contiguous(), dtype=od, checkpoint=few)
+            # other lanes per row, so other orders of the sums: either value is off by DEPTH u (E|x| + 2 |y|), with
+            # E|x| < 1 and |y| < 6, and rounded once
+            close(y[pick], f64(ys), 26 * DEPTH * U + half(od) * np.abs(f64(ys)), od)
+            assert torch.equal(ck.q[pick], few.q) and torch.equal(ck.scale[pick], few.scale)
+            assert guards(ob, n * cols, 1)
+            assert torch.equal(ma.act_pack(x).q, ck.q)
+            assert torch.equal(ma.act_unpack(ck, out=y)[pick], ma.act_unpack(few, dtype=od)) and guards(ob, n * cols, 1)
+            t = torch.randint(0, n, (n,), device=DEV, generator=torch.Generator(DEV).manual_seed(121))
+            assert torch.equal(ma.embedding_forward(x, t, out=y), x[t].to(od)) and guards(ob, n * cols, 1)
+        gb, g = view(torch.ones(n, cols, device=DEV), 1)
+        p = torch.randperm(n, device=DEV, generator=torch.Generator(DEV).manual_seed(122))[:5000]
+        ma.embedding_backward(x[:5000], p, g)
+        assert torch.equal(g[p], x[:5000].float()) and guards(gb, n * cols, 1)
+        g[p] = 0
+        assert not g.any()
+
+
 def test_training_step_end_to_end():
     """Embedding, norm with checkpoint, a linear layer, their gradients out of the checkpoints, and the optimizer
     step that reads them, against the same chain in fp64 from the stored values of each stage."""
