@@ -342,8 +342,8 @@ int ma_lion_step(const ma_lion_segment* segments, int32_t n_segments, void* stre
  * tensors are dense and row-major and start at any multiple of their element
  * size; outputs may not overlap any other buffer of the call
  * (MA_ERR_INVALID_ARG). Sums are fp32, in an order that depends on the sizes
- * alone, and each output is rounded once to its type: a call repeated on the
- * same inputs gives the same bits. accumulate = 1 adds to the gradient that is
+ * and types (and the tokens) alone, and each output is rounded once to its
+ * type: a call repeated on the same inputs gives the same bits. accumulate = 1 adds to the gradient that is
  * already there (in fp32, before the one rounding); 0 writes it whole. `stream`
  * must belong to the current device (MA_ERR_INVALID_ARG). Every call may be
  * captured in a HIP graph; a graph keeps the workspace it was captured with,
