@@ -375,6 +375,9 @@ int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* toke
  * cols <= 16384, rows * cols <= 2^36):
  *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
  *   y = (x - mean) * rstd * gain + bias        gain, bias: cols fp32 values, either may be null
+ * A mean of more than 4 deviations is corrected by the sum of the differences
+ * from it, so that a row of equal values has no variance. Sums are fp32: a row
+ * whose sum of squares passes its range has rstd 0, one whose sum does NaN.
  * stats (rows x 2 fp32, 8-byte aligned) receives mean and rstd for the backward
  * pass. With ckpt_q and ckpt_scale (both or neither) the same pass also writes
  * the 8-bit checkpoint of x, as ma_act_pack would. */

@@ -631,3 +631,33 @@ def test_training_step_end_to_end():
     touched = torch.from_numpy(count > 0).to(DEV)
     assert torch.isfinite(W1.float()).all() and not torch.equal(W1[0], W)
     assert torch.equal(table1[~touched], table[~touched]) and bool((table1[touched] != table[touched]).any(1).all())
+
+
+# ---------------------------------------------------------------------------
+# rows of equal values: the mean is the value itself, whatever 1 / cols rounds to
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows", [5, 600])
+@pytest.mark.parametrize("cols", [1, 3, 41, 82, 333, 1000, 1025, 2047, 4099, 8200, 16383])
+@pytest.mark.parametrize("xd,yd", [(F32, F32), (BF16, F32), (F32, BF16), (BF16, BF16)])
+def test_layernorm_of_equal_values(rows, cols, xd, yd):
+    """x - mean is a small multiple of x's step in every column, so its sum and the sum over cols are exact: the
+    corrected mean is x, the variance 0, y the bias and rstd that of eps alone."""
+    say("layernorm of equal values", rows, cols, xd, yd)
+    values = torch.tensor([0.5, 1000.1, -3.3e7, 1e-3, 1e15], device=DEV).to(xd)
+    x = values[torch.arange(rows, device=DEV) % 5, None].expand(rows, cols).contiguous()
+    bias, gain = rand((cols,), 130), 1 + rand((cols,), 131)
+    for eps in (1e-5, 1e-30):
+        y, stats = ma.layernorm_forward(x, gain, bias, eps=eps, dtype=yd)
+        assert torch.equal(stats[:, 0], x[:, 0].float())
+        assert torch.equal(y, bias.to(yd).expand(rows, cols))
+        want = 1.0 / np.sqrt(float(np.float32(eps)))
+        close(stats[:, 1], np.full(rows, want), 4 * U * want)   # (the reciprocal root: 2 units in the last place)
+
+
+def test_layernorm_mean_of_a_row_with_an_infinity():
+    """The mean of a row with an infinity is that infinity, also behind the correction of the mean."""
+    x = rand((4, 700), 132)
+    x[1, 5], x[3, 699] = float("inf"), float("-inf")
+    _, stats = ma.layernorm_forward(x)
+    assert stats[1, 0].item() == float("inf") and stats[3, 0].item() == float("-inf")
+    assert torch.isnan(stats[[1, 3], 1]).all() and torch.isfinite(stats[[0, 2]]).all()
