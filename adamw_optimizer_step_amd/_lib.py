@@ -115,6 +115,8 @@ EXPORTS = {
     "ma_test_muon_update": (C.c_int, [C.POINTER(MuonGroupC), C.c_void_p, C.c_int32, C.c_float,
                                       C.c_float, C.c_int32, C.c_int32, C.c_void_p]),
     "ma_test_fail_after_fork": (C.c_int, []),
+    "ma_test_act_weight_grad_plan": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.POINTER(C.c_int32),
+                                               C.POINTER(C.c_int32)]),
     "ma_test_ns_workspace_size": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int32, C.c_int32]),
     "ma_test_ns": (C.c_int, [C.c_int64, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
                              C.POINTER(C.c_float), C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),

@@ -268,6 +268,17 @@ size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t i
   return wgrad_workspace(wgrad_plan(tokens, outs, ins, dy_dtype).splits, outs, ins);
 }
 
+int ma_test_act_weight_grad_plan(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype, int32_t* edge, int32_t* splits) {
+  const char* fn = "ma_test_act_weight_grad_plan";
+  int rc;
+  if ((rc = wgrad_sizes(fn, tokens, outs, ins, dy_dtype))) return rc;
+  if (!edge || !splits) return fail(MA_ERR_INVALID_ARG, "%s: edge or splits is null", fn);
+  const WgradPlan plan = wgrad_plan(tokens, outs, ins, dy_dtype);
+  *edge = plan.big ? 256 : 128;
+  *splits = plan.splits;
+  return MA_OK;
+}
+
 int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const uint8_t* scale, int64_t tokens, int64_t outs, int64_t ins,
                        void* grad, int32_t grad_dtype, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "ma_act_weight_grad";

@@ -505,6 +505,12 @@ int ma_test_muon_update(const ma_muon_group* group, const void* u, int32_t u_dty
  * failure there would: for testing that the join is still enqueued. */
 int ma_test_fail_after_fork(void);
 
+/* What ma_act_weight_grad does with these sizes: the edge of its square output
+ * tile (128 or 256) and the number of contiguous shares of the tokens that
+ * are summed apart. Host only. */
+int ma_test_act_weight_grad_plan(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype,
+                                 int32_t* edge, int32_t* splits);
+
 /* Newton-Schulz iteration alone: `count` dense m x n matrices (m <= n) in
  * x0 (DEVICE, dtype `precision`), result in u (DEVICE, same layout). */
 size_t ma_test_ns_workspace_size(int64_t m, int64_t n, int32_t count, int32_t precision);

@@ -6,11 +6,14 @@ Error bounds are per element and follow from the operations: u = 2^-24 is half
 an fp32 step; a sum of n fp32 terms in any order is off by at most n u times the
 sum of the magnitudes (to first order); a result rounded once to type t is off
 by half a step more, eps(t) / 2 of its value."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
 
 import adamw_optimizer_step_amd as ma
+from adamw_optimizer_step_amd import _lib as L
 from gpu_util import need_gpu, say, to_np
 from oracle import train_ops as T
 
@@ -661,3 +664,87 @@ def test_layernorm_mean_of_a_row_with_an_infinity():
     _, stats = ma.layernorm_forward(x)
     assert stats[1, 0].item() == float("inf") and stats[3, 0].item() == float("-inf")
     assert torch.isnan(stats[[1, 3], 1]).all() and torch.isfinite(stats[[0, 2]]).all()
+
+
+# ---------------------------------------------------------------------------
+# both tiles of the weight gradient, each with one split of the tokens and with several: (tokens, outs, ins, edge of
+# the tile, splits or None for several, dy's types that take it there)
+# ---------------------------------------------------------------------------
+TILES = [
+    (5, 4090, 4081, 256, 1, (BF16, F32)), (65, 1030, 8200, 256, 1, (BF16, F32)), (130, 4096, 4096, 256, 1, (BF16, F32)),
+    (700, 4090, 4081, 256, 1, (BF16, F32)), (4099, 2050, 2041, 256, None, (BF16, F32)), (8192, 3000, 1000, 256, None, (BF16, F32)),
+    (1000, 2041, 2050, 256, None, (F32,)), (1000, 2050, 2041, 128, 1, (BF16,)), (63, 130, 300, 128, 1, (BF16,)),
+    (4096, 64, 128, 128, None, (BF16, F32)), (1000, 250, 333, 128, None, (BF16, F32)), (20, 250, 333, 128, 1, (BF16, F32)),
+]
+EVERY_TILE = [(*case[:5], dt) for case in TILES for dt in case[5]]
+
+
+def assert_tile(t, n, k, edge, splits, dyd):
+    e, s = C.c_int32(), C.c_int32()
+    L.check(L.lib().ma_test_act_weight_grad_plan(t, n, k, L.MA_F32 if dyd == F32 else L.MA_BF16, C.byref(e), C.byref(s)))
+    assert e.value == edge and (s.value > 1 if splits is None else s.value == splits), (e.value, s.value)
+
+
+def product(dy, x):
+    """dy^T x in fp64 on the device."""
+    return dy.double().t().contiguous() @ x.double()
+
+
+def close_on_device(got, want, tol, dtype):
+    """As `close`, of finite fp64 tensors."""
+    bound = tol * (1 + half(dtype)) + half(dtype) * want.abs() + torch.finfo(dtype).smallest_normal * half(dtype) * 2
+    assert bool(((got.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("t,n,k,edge,splits,dyd", EVERY_TILE)
+@pytest.mark.parametrize("gd,acc,off", [(F32, False, 1), (BF16, True, 0), (F32, True, 0), (BF16, False, 3)])
+def test_weight_grad_of_every_tile(t, n, k, edge, splits, dyd, gd, acc, off):
+    say("weight_grad tile", t, n, k, edge, splits, dyd, gd, acc, off)
+    assert_tile(t, n, k, edge, splits, dyd)
+    dy, x = rand((t, n), 140, dyd, 0.1), rand((t, k), 141, BF16)
+    x *= 2.0 ** torch.randint(-6, 6, (t, 1), device=DEV)
+    c = ma.act_pack(x)
+    held, g0 = ma.act_unpack(c), rand((n, k), 142, gd)
+    want, mag = product(dy, held), product(dy.abs(), held.abs())
+    _, dyv = view(dy, off)
+    gb, gv = view(g0, off)
+    ma.act_weight_grad(dyv, c, gv, accumulate=acc)
+    # as in test_weight_grad: t additions, three times as many for fp32 dy, 2 u each
+    tol = ((3 if dyd == F32 else 1) * t + 16) * 2 * U * mag
+    if acc:
+        want, tol = want + g0.double(), tol + U * (g0.double().abs() + mag)
+    close_on_device(gv, want, tol, gd)
+    assert guards(gb, n * k, off)
+    again = g0.clone()
+    ma.act_weight_grad(dy, c, again, accumulate=acc)
+    assert torch.equal(again, gv)
+
+
+@pytest.mark.parametrize("t,n,k,edge,splits,dyd", EVERY_TILE)
+def test_weight_grad_of_every_tile_is_exact_for_exact_sums(t, n, k, edge, splits, dyd):
+    """Small whole numbers: every sum is exact, so an element in a wrong place or counted twice shows."""
+    say("weight_grad tile, whole numbers", t, n, k, edge, splits, dyd)
+    assert_tile(t, n, k, edge, splits, dyd)
+    g = torch.Generator(DEV).manual_seed(t + n)
+    dy = torch.randint(-4, 5, (t, n), generator=g, device=DEV).to(dyd)
+    x = torch.randint(-8, 9, (t, k), generator=g, device=DEV).float()
+    got = ma.act_weight_grad(dy, ma.act_pack(x), torch.empty(n, k, device=DEV))
+    assert torch.equal(got.double(), product(dy, x))
+
+
+@pytest.mark.parametrize("t,n,k,edge,splits,dyd", [c for c in EVERY_TILE if c[0] >= 20 and c[2] >= 300])
+def test_weight_grad_of_every_tile_keeps_nonfinite_values_in_their_places(t, n, k, edge, splits, dyd):
+    """A NaN or infinity in dy reaches its own row of the gradient only, one in x its own column only."""
+    say("weight_grad tile, nonfinite", t, n, k, edge, splits, dyd)
+    assert_tile(t, n, k, edge, splits, dyd)
+    dy, x = rand((t, n), 143, dyd), rand((t, k), 144, BF16).abs() + 0.1
+    dy[t - 1, n - 1], dy[0, 7], x[3, k - 1] = float("inf"), float("nan"), float("nan")
+    got = ma.act_weight_grad(dy, ma.act_pack(x), torch.empty(n, k, device=DEV))
+    want = torch.ones(n, k, dtype=torch.bool, device=DEV)
+    want[n - 1], want[7], want[:, k - 1] = False, False, False
+    assert torch.equal(torch.isfinite(got), want)
+
+
+def test_both_tiles_ran_with_one_split_and_with_several():
+    ran = {(edge, splits == 1, dyd) for _, _, _, edge, splits, dyd in EVERY_TILE}
+    assert len(ran) == 8

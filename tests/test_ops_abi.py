@@ -153,3 +153,23 @@ def test_binding_rejects_host_tensors():
               lambda: ma.act_weight_grad(torch.zeros(4, 6), c, torch.zeros(6, 8))):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def plan(t, n, k, dt):
+    e, s = C.c_int32(-1), C.c_int32(-1)
+    assert L.lib().ma_test_act_weight_grad_plan(t, n, k, dt, C.byref(e), C.byref(s)) == 0
+    return e.value, s.value
+
+
+def test_weight_grad_plan_query():
+    """The query says what the workspace sizes say, and rejects what they reject."""
+    for t, n, k in ((0, 4, 4), (1, 1, 1), (1000, 250, 333), (4099, 2050, 2041), (12288, 16384, 4096), (700, 4090, 4081), (63, 130, 300)):
+        for dt, name in ((L.MA_F32, torch.float32), (L.MA_BF16, torch.bfloat16)):
+            edge, splits = plan(t, n, k, dt)
+            assert edge in (128, 256) and splits >= 1
+            assert ma.act_weight_grad_workspace_size(t, n, k, name) == (0 if splits == 1 else splits * -(-n * k // 64) * 64 * 4)
+    assert plan(12288, 16384, 4096, L.MA_BF16) == (256, 1) and plan(63, 130, 300, L.MA_BF16) == (128, 1)
+    e = C.c_int32()
+    f = L.lib().ma_test_act_weight_grad_plan
+    assert f(-1, 4, 4, 0, C.byref(e), C.byref(e)) == INV and f(4, 0, 4, 0, C.byref(e), C.byref(e)) == INV
+    assert f(4, 4, 4, 2, C.byref(e), C.byref(e)) == UNS and f(4, 4, 4, 0, None, C.byref(e)) == INV and f(4, 4, 4, 0, C.byref(e), None) == INV
