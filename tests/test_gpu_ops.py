@@ -748,3 +748,13 @@ def test_weight_grad_of_every_tile_keeps_nonfinite_values_in_their_places(t, n, 
 def test_both_tiles_ran_with_one_split_and_with_several():
     ran = {(edge, splits == 1, dyd) for _, _, _, edge, splits, dyd in EVERY_TILE}
     assert len(ran) == 8
+
+
+# ---------------------------------------------------------------------------
+# more than 1024 rows of more than 8192 columns: operands read twice, and partial sums
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,cols", [(1030, 8200), (1100, 16383), (1025, 16384)])
+@pytest.mark.parametrize("kind,dyd,affine,off", [("f32", F32, True, 0), ("bf16", BF16, True, 1), ("ckpt", F32, False, 1), ("ckpt", BF16, True, 0)])
+def test_layernorm_backward_of_many_wide_rows(rows, cols, kind, dyd, affine, off):
+    assert ma.layernorm_workspace_size(rows, cols) > 0
+    test_layernorm_backward(rows, cols, kind, dyd, affine, off)
