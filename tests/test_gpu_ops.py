@@ -758,3 +758,26 @@ def test_both_tiles_ran_with_one_split_and_with_several():
 def test_layernorm_backward_of_many_wide_rows(rows, cols, kind, dyd, affine, off):
     assert ma.layernorm_workspace_size(rows, cols) > 0
     test_layernorm_backward(rows, cols, kind, dyd, affine, off)
+
+
+# ---------------------------------------------------------------------------
+# token ids that only their upper 32 bits, or the sign of the lower ones, keep out of the table
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,cols,n", [(50, 24, 5), (300, 40, 64), (300, 40, 700), (97, 530, 1024), (97, 530, 1025),
+                                         (1000, 72, 5003), (300, 16, 16384), (700, 8, 40000)])
+@pytest.mark.parametrize("acc", [False, True])
+def test_embedding_gradient_of_far_tokens(rows, cols, n, acc):
+    say("embedding gradient of far tokens", rows, cols, n, acc)
+    g = torch.Generator().manual_seed(150)
+    r, d = torch.randint(0, rows, (n,), generator=g), rand((n, cols), 151)
+    far = torch.tensor([0, 1 << 32, 1 << 40, -(1 << 32), -(1 << 40), (1 << 31) - rows, 1 << 31, 3 << 30, -(1 << 63)])
+    which = torch.randint(0, 9, (n,), generator=g)
+    which[::3] = 0
+    t = r + far[which]
+    d[(t != r).to(DEV)] = float("nan")              # what is ignored is not read
+    g0 = rand((rows, cols), 152)
+    got = ma.embedding_backward(d, t.to(DEV), g0.clone(), accumulate=acc)
+    want, mag, count = T.embedding_backward(np.nan_to_num(f64(d)), t.numpy(), rows, 1.0, f64(g0) if acc else None)
+    assert 0 < count.sum() < n
+    # as in test_embedding_backward
+    close(got, want, (count[:, None] * (1 + 1 / 64) + 3) * U * mag + (U * (np.abs(f64(g0)) + mag) if acc else 0))
