@@ -1,6 +1,7 @@
 // C ABI of the operators around the optimizer step (embedding, layer norm,
 // 8-bit activation checkpoints, weight gradient): argument validation and the
 // launches. See include/muon_adamw.h for the contract of every entry point.
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/muon_adamw.h"
@@ -114,7 +115,9 @@ int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, i
 
 size_t ma_embedding_workspace_size(int64_t rows, int64_t cols, int64_t n_tokens) {
   if (embedding_sizes("ma_embedding_workspace_size", rows, cols, n_tokens)) return 0;
-  return embed_bwd_workspace(rows, cols, n_tokens);
+  // short pieces take more room than long ones of somewhat more tokens
+  const size_t need = embed_bwd_workspace(rows, cols, n_tokens);
+  return n_tokens > kEmbedShortPieces ? std::max(need, embed_bwd_workspace(rows, cols, kEmbedShortPieces)) : need;
 }
 
 int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t rows,

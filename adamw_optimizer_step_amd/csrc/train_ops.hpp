@@ -23,7 +23,8 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hip
 // sorted positions, one wave each, and joined in order. Short pieces shorten the
 // longest wave, long ones the join (5003 tokens x 333 fp32: sums 7.5 us with 16,
 // 10.5 with 32, join 4.2 both; 49152 x 1024 bf16: join 10.3 and 7.3, sums alike).
-constexpr int embed_piece(int64_t n_tokens) { return n_tokens <= 16384 ? 16 : 32; }
+constexpr int64_t kEmbedShortPieces = 16384;   // tokens
+constexpr int embed_piece(int64_t n_tokens) { return n_tokens <= kEmbedShortPieces ? 16 : 32; }
 // Up to this many tokens the rows' waves look for their tokens themselves, in
 // one launch in place of three (bf16 into 1000 x 1024: 1000 tokens 15 us against
 // 5.8 + 8.5 + 3.7 and two launches, 2000 tokens 24 against 6 + 8.2 + 4.6; into

@@ -118,6 +118,7 @@ def embedding_forward(table: torch.Tensor, tokens: torch.Tensor, scale: float = 
 
 
 def embedding_workspace_size(rows: int, cols: int, n_tokens: int) -> int:
+    """Bytes of workspace for at most ``n_tokens`` tokens."""
     n = L.lib().ma_embedding_workspace_size(rows, cols, n_tokens)
     if n == 0:
         L.check(L.MA_ERR_INVALID_ARG)
@@ -295,7 +296,7 @@ def layernorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, bias
 
 
 def layernorm_workspace_size(rows: int, cols: int) -> int:
-    """Bytes of workspace (0: none needed)."""
+    """Bytes of workspace (0: none needed) for at most ``rows`` rows."""
     n = L.lib().ma_layernorm_workspace_size(rows, cols)
     if n == 0 and not (0 <= rows <= 1 << 24 and 1 <= cols <= 16384 and rows * cols <= 1 << 36):
         L.check(L.MA_ERR_INVALID_ARG)
@@ -344,7 +345,9 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
 # weight gradient
 # ---------------------------------------------------------------------------
 def act_weight_grad_workspace_size(tokens: int, outs: int, ins: int, dtype: torch.dtype = torch.bfloat16) -> int:
-    """Bytes of workspace (0: none needed) for dy of ``dtype``."""
+    """Bytes of workspace (0: none needed) for dy of ``dtype`` and exactly these
+    sizes: fewer tokens can need more, so a workspace for calls of several
+    sizes takes the largest of theirs."""
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
     n = L.lib().ma_act_weight_grad_workspace_size(tokens, outs, ins, _DT[dtype])

@@ -365,7 +365,8 @@ int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, i
  * rows x cols, fp32. The tokens are sorted first (stable, by kernels of this
  * call): short runs are summed in ascending i, longer ones in pieces that are
  * joined in order. workspace: at least ma_embedding_workspace_size bytes
- * (0 from that function: invalid sizes), MA_WORKSPACE_ALIGN aligned. */
+ * (0 from that function: invalid sizes), MA_WORKSPACE_ALIGN aligned; that of
+ * more tokens serves fewer too. */
 size_t ma_embedding_workspace_size(int64_t rows, int64_t cols, int64_t n_tokens);
 int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* tokens, int32_t token_bytes, int64_t n_tokens,
                           int64_t rows, int64_t cols, float scale, int32_t accumulate, float* grad, void* workspace,
@@ -391,8 +392,8 @@ int ma_layernorm_forward(const void* x, int32_t x_dtype, int64_t rows, int64_t c
  *   dgain (+)= sum over rows of dy * xh;  dbias (+)= sum over rows of dy
  * dx has x's type, or dy's where x is a checkpoint. dgain and dbias (cols fp32
  * values) may each be null; with both null no workspace is needed, else at
- * least ma_layernorm_workspace_size bytes, which may be 0 (few rows). accumulate
- * applies to dgain and dbias. */
+ * least ma_layernorm_workspace_size bytes, which may be 0 (few rows); that of
+ * more rows serves fewer too. accumulate applies to dgain and dbias. */
 size_t ma_layernorm_workspace_size(int64_t rows, int64_t cols);
 int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const uint8_t* ckpt_q,
                           const uint8_t* ckpt_scale, int64_t rows, int64_t cols, const float* stats, const float* gain,
@@ -422,7 +423,10 @@ int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
  * second rounding) and dy at its full precision; products are summed in fp32.
  * Limits: tokens <= 2^25, outs, ins <= 2^23, outs * ins <= 2^31, tokens * outs and
  * tokens * P <= 2^36. workspace: at
- * least ma_act_weight_grad_workspace_size bytes, which may be 0. */
+ * least ma_act_weight_grad_workspace_size bytes, which may be 0. That is the
+ * need of exactly these sizes: fewer tokens can need more (they may be shared
+ * out among more blocks), so a workspace for calls of several sizes takes the
+ * largest of theirs. */
 size_t ma_act_weight_grad_workspace_size(int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype);
 int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const uint8_t* scale, int64_t tokens,
                        int64_t outs, int64_t ins, void* grad, int32_t grad_dtype, int32_t accumulate, void* workspace,

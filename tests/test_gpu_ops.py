@@ -781,3 +781,15 @@ def test_embedding_gradient_of_far_tokens(rows, cols, n, acc):
     assert 0 < count.sum() < n
     # as in test_embedding_backward
     close(got, want, (count[:, None] * (1 + 1 / 64) + 3) * U * mag + (U * (np.abs(f64(g0)) + mag) if acc else 0))
+
+
+@pytest.mark.parametrize("rows,cols", [(1000, 40), (50304, 24)])
+def test_embedding_workspace_serves_fewer_tokens_too(rows, cols):
+    """One workspace, of the size for the longest batch, for every shorter one."""
+    longest = 20000
+    ws = torch.empty(ma.embedding_workspace_size(rows, cols, longest), dtype=torch.uint8, device=DEV)
+    t, d = tokens("zipf", rows, longest, 160).to(DEV), rand((longest, cols), 161, BF16)
+    for n in (longest, 16385, 16384, 3000, 1025, 1024, 5):
+        say("embedding workspace", rows, cols, n)
+        got = ma.embedding_backward(d[:n], t[:n], torch.empty(rows, cols, device=DEV), workspace=ws)
+        assert torch.equal(got, ma.embedding_backward(d[:n], t[:n], torch.empty(rows, cols, device=DEV)))

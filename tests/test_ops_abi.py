@@ -173,3 +173,16 @@ def test_weight_grad_plan_query():
     f = L.lib().ma_test_act_weight_grad_plan
     assert f(-1, 4, 4, 0, C.byref(e), C.byref(e)) == INV and f(4, 0, 4, 0, C.byref(e), C.byref(e)) == INV
     assert f(4, 4, 4, 2, C.byref(e), C.byref(e)) == UNS and f(4, 4, 4, 0, None, C.byref(e)) == INV and f(4, 4, 4, 0, C.byref(e), None) == INV
+
+
+def test_embedding_workspace_of_more_tokens_serves_fewer():
+    """The size never falls with the tokens, past the changes of the pieces' length and of the form too."""
+    for rows, cols in ((1, 1), (1000, 40), (50304, 1024), (1 << 18, 3)):
+        sizes = [ma.embedding_workspace_size(rows, cols, n) for n in (0, 1, 1024, 1025, 3000, 16383, 16384, 16385, 20000, 30000, 32768, 32769, 49152, 1 << 20)]
+        assert sizes == sorted(sizes)
+
+
+def test_layernorm_workspace_of_more_rows_serves_fewer():
+    for cols in (1, 700, 1500, 2047, 4096, 8192, 16384):
+        sizes = [ma.layernorm_workspace_size(rows, cols) for rows in [*range(0, 3000, 7), 4096, 5000, 20000, 49152, 1 << 20]]
+        assert sizes == sorted(sizes)
