@@ -133,7 +133,7 @@ int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* toke
                       {tokens, n_tokens * token_bytes, token_bytes, false, false, "tokens"},
                       {grad, rows * cols * 4, 4, true, false, "grad"},
                       {workspace, (int64_t)need, 1, true, true, "the workspace"}};
-  if ((rc = check_buffers(fn, bufs)) || (rc = check_workspace(fn, workspace, workspace_bytes, need))) return rc;
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, need)) || (rc = check_buffers(fn, bufs))) return rc;
   if (n_tokens == 0 && accumulate) return MA_OK;
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -215,7 +215,7 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
                       {dgain, cols * 4, 4, true, true, "dgain"},
                       {dbias, cols * 4, 4, true, true, "dbias"},
                       {workspace, (int64_t)need, 1, true, true, "the workspace"}};
-  if ((rc = check_buffers(fn, bufs)) || (rc = check_workspace(fn, workspace, workspace_bytes, need))) return rc;
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, need)) || (rc = check_buffers(fn, bufs))) return rc;
   if (rows == 0 && (!sums || accumulate)) return MA_OK;
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -296,7 +296,7 @@ int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const
                       {scale, tokens * (pitch / kActBlock), 1, false, false, "scale"},
                       {grad, outs * ins * dt_size(grad_dtype), (int)dt_size(grad_dtype), true, false, "grad"},
                       {workspace, (int64_t)need, 1, true, true, "the workspace"}};
-  if ((rc = check_buffers(fn, bufs)) || (rc = check_workspace(fn, workspace, workspace_bytes, need))) return rc;
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, need)) || (rc = check_buffers(fn, bufs))) return rc;
   if (tokens == 0 && accumulate) return MA_OK;
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);

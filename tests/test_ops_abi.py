@@ -186,3 +186,12 @@ def test_layernorm_workspace_of_more_rows_serves_fewer():
     for cols in (1, 700, 1500, 2047, 4096, 8192, 16384):
         sizes = [ma.layernorm_workspace_size(rows, cols) for rows in [*range(0, 3000, 7), 4096, 5000, 20000, 49152, 1 << 20]]
         assert sizes == sorted(sizes)
+
+
+def test_a_workspace_that_is_too_small_is_named_as_such():
+    """Also where the room it lacks belongs to another buffer of the call."""
+    for name, kw in (("ma_embedding_backward", dict(n_tokens=5000, grad=at(3) + 256)),
+                     ("ma_layernorm_backward", dict(rows=2000, workspace=at(3), dgain=at(3) + 256)),
+                     ("ma_act_weight_grad", dict(workspace=at(4), grad=at(4) + 256))):
+        assert call(name, workspace_bytes=256, **kw) == WS
+        assert b"256 bytes" in L.lib().ma_last_error()
