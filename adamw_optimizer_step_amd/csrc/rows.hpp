@@ -353,11 +353,6 @@ __device__ __forceinline__ void act_encode(const float (&v)[E], int e, uint32_t 
     q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * i + 2], t[4 * i + 3], b, true);
   }
 }
-__device__ __forceinline__ uint2 act_encode(const float (&v)[8], int e) {
-  uint32_t q[2];
-  act_encode<8>(v, e, q);
-  return make_uint2(q[0], q[1]);
-}
 
 __device__ __forceinline__ float act_scale(uint32_t b) { return __uint_as_float(b << 23); }
 
