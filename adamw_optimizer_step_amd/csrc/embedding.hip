@@ -1,7 +1,10 @@
 // Embedding lookup with scaling, and its gradient by sorted tokens (gfx950).
 //
 //   forward   out[i,:]  = RNE(scale * table[t_i,:])
-//   backward  grad[v,:] (+)= scale * sum over { i : t_i = v }, i ascending, of dout[i,:]
+//   backward  grad[v,:] (+)= scale * sum over { i : t_i = v } of dout[i,:]
+//
+// Few positions are summed in ascending i, more in contiguous parts that are added
+// in order: the same tokens give the same bits.
 //
 // A token outside [0, rows) is ignored: its output row is zero and no gradient
 // comes of it (a row of another shard, a masked position).

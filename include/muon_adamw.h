@@ -362,9 +362,12 @@ int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, i
 /* grad[v,:] = scale * sum of dout[i,:] over the i with tokens[i] == v, for
  * every row v < rows (zero where there is none). With accumulate the rows that
  * occur are added to and no other row is touched. dout: n_tokens x cols; grad:
- * rows x cols, fp32. The tokens are sorted first (stable, by kernels of this
- * call): short runs are summed in ascending i, longer ones in pieces that are
- * joined in order. workspace: at least ma_embedding_workspace_size bytes
+ * rows x cols, fp32. Up to 1024 tokens a row's positions are found by
+ * comparison, up to 16 of them summed in ascending i, more in 8 contiguous
+ * shares that are added in order. More tokens are sorted first (stable, by
+ * kernels of this call): runs of up to 16 positions (32 above 16384 tokens) are
+ * summed in ascending i, longer ones in pieces of as many sorted positions,
+ * whose sums are added up in 8 contiguous shares, in order. workspace: at least ma_embedding_workspace_size bytes
  * (0 from that function: invalid sizes), MA_WORKSPACE_ALIGN aligned; that of
  * more tokens serves fewer too. */
 size_t ma_embedding_workspace_size(int64_t rows, int64_t cols, int64_t n_tokens);
