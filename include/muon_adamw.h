@@ -423,7 +423,9 @@ int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
  *   grad[n,k] (+)= sum over tokens t of dy[t,n] * x[t,k]
  * dy: tokens x outs; q, scale: the checkpoint of x (tokens x ins) as written by
  * ma_act_pack; grad: outs x ins. The held values are used as they are (no
- * second rounding) and dy at its full precision; products are summed in fp32.
+ * second rounding) and dy at its full precision, but for what of a fp32 value
+ * lies below 2^-133, the last bit of bf16 (so all of it from 2^-110 up);
+ * products are summed in fp32.
  * Limits: tokens <= 2^25, outs, ins <= 2^23, outs * ins <= 2^31, tokens * outs and
  * tokens * P <= 2^36. workspace: at
  * least ma_act_weight_grad_workspace_size bytes, which may be 0. That is the

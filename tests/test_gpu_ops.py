@@ -793,3 +793,17 @@ def test_embedding_workspace_serves_fewer_tokens_too(rows, cols):
         say("embedding workspace", rows, cols, n)
         got = ma.embedding_backward(d[:n], t[:n], torch.empty(rows, cols, device=DEV), workspace=ws)
         assert torch.equal(got, ma.embedding_backward(d[:n], t[:n], torch.empty(rows, cols, device=DEV)))
+
+
+def test_weight_grad_of_small_fp32_dy():
+    """dy against one-hot activations is all there from 2^-110 up; below, what three terms of bf16 leave is under
+    2^-133, bf16's least number, whose multiples add up exactly in fp32."""
+    t, g = 96, torch.Generator().manual_seed(170)
+    m = (1 + torch.rand(t, 70, generator=g, dtype=torch.float64)) * torch.where(torch.rand(t, 70, generator=g) < 0.5, -1.0, 1.0)
+    for s in (0, 60):
+        c = ma.act_pack(torch.eye(t, device=DEV) * 2.0 ** s)
+        for e in (-90, -105, -110, -112, -118, -124, -126, -128, -132):
+            dy = (m * 2.0 ** e).float()
+            got = ma.act_weight_grad(dy.to(DEV), c, torch.empty(70, t, device=DEV)).cpu().double() * 2.0 ** -s
+            off = (got - dy.t().double()).abs()
+            assert not off.any() if e >= -110 else bool((off < 2.0 ** -133).all()), (s, e)
