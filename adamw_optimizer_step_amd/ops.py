@@ -7,6 +7,11 @@ computation runs in the HIP kernels of ``libmuon_adamw.so``, on the current
 stream of the tensors' device or on ``stream``. Tensors are contiguous; results
 that are not passed in are allocated for that stream. Names follow the C ABI
 (include/muon_adamw.h), which states each operator's rounding and limits.
+
+As the steps, the operators stand outside autograd: inputs are read as data,
+whether they require grad or not, results have no graph and no forward-mode
+tangent, and the caller runs the backward calls. Between them and autograd
+stands a ``torch.autograd.Function`` of the caller's.
 """
 from __future__ import annotations
 

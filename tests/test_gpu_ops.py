@@ -807,3 +807,36 @@ def test_weight_grad_of_small_fp32_dy():
             got = ma.act_weight_grad(dy.to(DEV), c, torch.empty(70, t, device=DEV)).cpu().double() * 2.0 ** -s
             off = (got - dy.t().double()).abs()
             assert not off.any() if e >= -110 else bool((off < 2.0 ** -133).all()), (s, e)
+
+
+def test_operators_stand_outside_autograd():
+    """Inputs that require grad are read as data: the same bits, no graph, no gradient. In a Function of the caller's
+    the backward calls give the gradients that autograd then passes on."""
+    w, t, gain = rand((40, 96), 180), tokens("spread", 40, 50, 181).to(DEV), 1 + rand((96,), 182, F32, 0.1)
+    plain = ma.embedding_forward(w, t)
+    want, stats = ma.layernorm_forward(plain, gain)
+    wg, gg = w.clone().requires_grad_(), gain.clone().requires_grad_()
+    x = ma.embedding_forward(wg, t)
+    y, _ = ma.layernorm_forward(x, gg)
+    assert torch.equal(x, plain) and torch.equal(y, want) and not x.requires_grad and not y.requires_grad
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, w, gain):
+            x = ma.embedding_forward(w, t)
+            y, stats = ma.layernorm_forward(x, gain)
+            ctx.save_for_backward(x, stats, gain)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, stats, gain = ctx.saved_tensors
+            dgain = torch.empty_like(gain)
+            dx = ma.layernorm_backward(dy.contiguous(), x, stats, gain, dgain=dgain)
+            return ma.embedding_backward(dx, t, torch.empty_like(w)), dgain
+
+    dy = rand((50, 96), 183)
+    Norm.apply(wg, gg).backward(dy)
+    dgain = torch.empty_like(gain)
+    dx = ma.layernorm_backward(dy, plain, stats, gain, dgain=dgain)
+    assert torch.equal(gg.grad, dgain) and torch.equal(wg.grad, ma.embedding_backward(dx, t, torch.empty_like(w)))
