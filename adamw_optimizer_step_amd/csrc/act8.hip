@@ -2,9 +2,10 @@
 // A group of 16 lanes holds one block of 128 columns of one row, 8 values per
 // lane, so that its amax takes four lane exchanges; 4 blocks per group in flight.
 // fp32 goes by 4 values per lane and 32 lanes per block (rows.hpp, quad_load_row).
-// HBM-bound: 24576 x 4096 bf16 (302 MB each way) packs in 48 us (6.3 TB/s) and
-// unpacks in 47 us. Packing reads x non-temporally where kStreamBytes says so (63
-// us without); unpacking always does for q, which is read once (60 us without).
+// HBM-bound: 24576 x 4096 bf16 (302 MB each way) packs in 49 us (6.2 TB/s) and
+// unpacks in 47 us in turn with packing, 55 behind one another. Packing reads x
+// non-temporally where kStreamBytes says so (56 to 63 us without); unpacking always
+// does for q, which is read once (60 us without, where it takes 47).
 #include "rows.hpp"
 #include "train_ops.hpp"
 

@@ -10,10 +10,13 @@ namespace ma {
 // cache beside anything else: they mark the larger of what they pass through as
 // non-temporal, so that it does not push out what the rest of the call, or the
 // next one, can still find there. Below it they leave the cache to the next
-// call. (Packing 24576 x 4096 bf16, 302 MB: 48 us with x loaded non-temporally, 63
-// without; layer norm of 24576 x 2048 bf16 with its checkpoint, 252 MB: 52.5 with y
-// stored so, 55 without; of 32768 x 1024, 134 MB, a pass over y after it takes 22
-// against 19.5.)
+// call. (Packing 24576 x 4096 bf16, 302 MB: 49 us with x loaded non-temporally, 56
+// without; layer norm of 24576 x 2048 bf16 with its checkpoint, 252 MB: 50 with y
+// stored so, 53 without; of 32768 x 1024, 134 MB, 23.5 against 25, but 53.5 against
+// 46 together with a pass over y after it.)
+// Three operands are loaded non-temporally whatever the size, as what the call reads
+// for the last time: a checkpoint's q in unpacking and in norm's backward pass, x in
+// that pass, and the embedding gradient's dout. Measured on large calls only.
 constexpr int64_t kStreamBytes = (int64_t)192 << 20;
 
 // A 16-byte access at 2- or 4-byte alignment: gfx950 serves it as one

@@ -7,10 +7,10 @@
 // summed in the same accumulators.
 //
 // Bound by the matrix instructions where tokens and outputs are many: 12288 x
-// (16384 x 4096) bf16 in 1.23 to 1.29 ms, 1.28 to 1.34 PFLOP/s at the 1.74 GHz that
-// the card holds under this load, the matrix units busy 70 % of it. A plain library
-// product of the unpacked operands in this layout reaches 1.24 PFLOP/s, of
-// contiguous ones 1.43. fp32 dy, three products: 8192 x (2048 x 2048) 166 us + 14
+// (16384 x 4096) bf16 in 1.23 to 1.34 ms (medians of several runs and cards), 1.23 to
+// 1.34 PFLOP/s at the 1.75 GHz that the card holds under this load, the matrix units
+// busy 71 % of it. A plain library product of the unpacked operands in this layout
+// reaches 1.24 PFLOP/s, of contiguous ones 1.43. fp32 dy, three products: 8192 x (2048 x 2048) 166 us + 14
 // for the join (1.2 PFLOP/s of bf16 products).
 #include "rows.hpp"
 #include "train_ops.hpp"
