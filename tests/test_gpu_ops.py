@@ -840,3 +840,73 @@ def test_operators_stand_outside_autograd():
     dgain = torch.empty_like(gain)
     dx = ma.layernorm_backward(dy, plain, stats, gain, dgain=dgain)
     assert torch.equal(gg.grad, dgain) and torch.equal(wg.grad, ma.embedding_backward(dx, t, torch.empty_like(w)))
+
+
+# ---------------------------------------------------------------------------
+# the largest rows and columns that each operator takes, with few of the other
+# ---------------------------------------------------------------------------
+def whole(shape, seed, dtype, most=4):
+    """Small whole numbers, whose sums are exact."""
+    return torch.randint(-most, most + 1, shape, generator=torch.Generator(DEV).manual_seed(seed), device=DEV).to(dtype)
+
+
+@pytest.mark.parametrize("n", [900, 1500])
+def test_largest_table(n):
+    rows = 1 << 24
+    say("largest table", n)
+    w = rand((rows, 2), 190)
+    t = 1 + torch.randperm(rows - 2, generator=torch.Generator(DEV).manual_seed(191), device=DEV)[:n]
+    t[0], t[1] = rows - 1, 0
+    assert torch.equal(ma.embedding_forward(w, t), w[t])
+    d = rand((n, 2), 192)
+    g = ma.embedding_backward(d, t, torch.empty_like(w))
+    assert torch.equal(g[t], d)
+    g[t] = 0
+    assert not g.any()
+
+
+@pytest.mark.parametrize("n", [20, 1030])
+def test_widest_table(n):
+    cols = 1 << 20
+    say("widest table", n)
+    w, t = whole((3, cols), 193, BF16), torch.randint(0, 3, (n,), generator=torch.Generator(DEV).manual_seed(194), device=DEV)
+    assert torch.equal(ma.embedding_forward(w, t[:20], dtype=F32), w[t[:20]].float())
+    d = whole((n, cols), 195, BF16)
+    g = ma.embedding_backward(d, t, torch.empty(3, cols, device=DEV))
+    for v in range(3):
+        assert torch.equal(g[v], d[t == v].float().sum(0))
+
+
+def test_most_norm_rows():
+    rows = 1 << 24
+    say("most norm rows")
+    x = rand((rows, 3), 196, BF16)
+    y, stats = ma.layernorm_forward(x)
+    for part in (slice(0, 700), slice(rows - 700, rows)):
+        ys, ss = ma.layernorm_forward(x[part].contiguous())
+        assert torch.equal(y[part], ys) and torch.equal(stats[part], ss)
+    db = torch.empty(3, device=DEV)
+    dx = ma.layernorm_backward(torch.ones_like(x), x, stats, dbias=db)
+    assert bool((db == rows).all()) and not dx.isnan().any()
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 1 << 24), (1 << 24, 1)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_largest_checkpoints(rows, cols, dt):
+    say("largest checkpoints", rows, cols, dt)
+    x = whole((rows, cols), 197, dt, 8)
+    assert torch.equal(ma.act_unpack(ma.act_pack(x), dtype=dt), x)
+
+
+@pytest.mark.parametrize("n,k", [(1 << 23, 1), (1, 1 << 23), (1 << 23, 200)])
+@pytest.mark.parametrize("dyd", [F32, BF16])
+def test_largest_weight_gradients(n, k, dyd):
+    say("largest weight gradients", n, k, dyd)
+    t = 70
+    dy, x = whole((t, n), 198, dyd), whole((t, k), 199, BF16, 8)
+    got = ma.act_weight_grad(dy, ma.act_pack(x), torch.empty(n, k, device=DEV))
+    for part in (slice(0, 5000), slice(max(n, k) - 5000, None)):
+        if n > k:
+            assert torch.equal(got[part].double(), product(dy[:, part], x))
+        else:
+            assert torch.equal(got[:, part].double(), product(dy, x[:, part]))
