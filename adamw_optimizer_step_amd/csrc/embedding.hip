@@ -115,7 +115,8 @@ hipError_t launch_embed_fwd(const EmbedFwdArgs& a, int table_dt, int out_dt, hip
 //
 // Every block reads every token, from its XCD's L2: what a block does per 64
 // tokens (a load, a compare, two ballots) bounds it, not memory. 49152 tokens of
-// 50304 rows: 15 us; 5003: 6.6, mostly its chain of waits; all in one row: 81.
+// 50304 rows: 15 us; 5003: 6.6, mostly its chain of waits; all in one row: 81; 2^20
+// evenly spread: 146; with Zipf's frequencies, where lists overflow: 1716.
 // ---------------------------------------------------------------------------
 constexpr int kBinThreads = 1024, kBinWaves = kBinThreads / 64, kBinRows = 512, kBinBits = 9, kBinList = 1024;
 
