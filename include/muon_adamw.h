@@ -367,9 +367,9 @@ int ma_embedding_forward(const void* table, int32_t table_dtype, int64_t rows, i
  * shares that are added in order. More tokens are sorted first (stable, by
  * kernels of this call): runs of up to 16 positions (32 above 16384 tokens) are
  * summed in ascending i, longer ones in pieces of as many sorted positions,
- * whose sums are added up in 8 contiguous shares, in order. workspace: at least ma_embedding_workspace_size bytes
- * (0 from that function: invalid sizes), MA_WORKSPACE_ALIGN aligned; that of
- * more tokens serves fewer too. */
+ * whose sums are added up in 8 contiguous shares, in order. workspace: at
+ * least ma_embedding_workspace_size bytes (0 from that function: invalid
+ * sizes), MA_WORKSPACE_ALIGN aligned; that of more tokens serves fewer too. */
 size_t ma_embedding_workspace_size(int64_t rows, int64_t cols, int64_t n_tokens);
 int ma_embedding_backward(const void* dout, int32_t dout_dtype, const void* tokens, int32_t token_bytes, int64_t n_tokens,
                           int64_t rows, int64_t cols, float scale, int32_t accumulate, float* grad, void* workspace,
