@@ -8,6 +8,7 @@ operations, or, where `own` is true, by this package's kernels.
 Held in 4 bits: per row and block of 32 columns, e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one
 power of two 2^e, e the least exponent (-126 .. 125) for which amax / 2^e rounds to at most 6; the scale byte is
 e + 127, two values share a byte (the even column the lower half), rows are padded to whole blocks of 128 with zeros.
+The scale bytes lie as [columns / 128, rows, 4].
 
 Held in 8 bits: per row and block of 128 columns, e4m3 values and one power of two 2^e, e the least exponent
 (-117 .. 120) with amax <= 448 * 2^e; the scale byte is e + 127.
@@ -136,11 +137,13 @@ def _pack4(x):
     code = (code + 8 * torch.signbit(v)).to(torch.uint8).view(x.shape[0], -1)
     bad = ~amax.isfinite()
     code = torch.where(bad.repeat_interleave(32, 1), 0, code).to(torch.uint8)
-    return code[:, ::2] | code[:, 1::2] << 4, torch.where(bad, 255, e + 127).to(torch.uint8)
+    scale = torch.where(bad, 255, e + 127).to(torch.uint8)
+    return code[:, ::2] | code[:, 1::2] << 4, scale.view(x.shape[0], -1, 4).transpose(0, 1).contiguous()
 
 
 def _unpack4(q, scale, cols):
     values = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], device=q.device)
+    scale = scale.transpose(0, 1).reshape(q.shape[0], -1)
     v = values[torch.stack([q & 15, q >> 4], -1).long()].view(*scale.shape, 32)
     s = torch.ldexp(torch.ones_like(scale, dtype=torch.float32), scale.int() - 127)
     s = torch.where(scale == 255, float("nan"), s)
@@ -289,6 +292,7 @@ def _value8(q, scale, cols):
 
 def _value4(q, scale, cols):
     """sign, 2 bits of exponent with bias 1, 1 of fraction"""
+    scale = scale.permute(1, 0, 2).flatten(1)
     q = torch.stack([q % 16, q // 16], 2).flatten(1).long()
     e, f = (q % 8) // 2, (q % 2).double()
     v = torch.where(e > 0, (2 + f) * torch.exp2(e.double() - 2), f / 2)
