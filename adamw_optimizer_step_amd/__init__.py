@@ -10,8 +10,9 @@ from .api import (  # noqa: F401
     newton_schulz, optimizer_step, update_stage,
 )
 from .ops import (  # noqa: F401
-    ActCheckpoint, act_pack, act_unpack, act_weight_grad, act_weight_grad_workspace_size, embedding_backward,
+    ActCheckpoint, Mx4Matrix, act_pack, act_unpack, act_weight_grad, act_weight_grad_workspace_size, embedding_backward,
     embedding_forward, embedding_workspace_size, layernorm_backward, layernorm_forward, layernorm_workspace_size,
+    mx4_matmul, mx4_matmul_workspace_size, mx4_pack, mx4_unpack, rmsnorm_backward, rmsnorm_forward, rmsnorm_workspace_size,
 )
 from ._lib import MuonAdamWError, lib  # noqa: F401
 from .coefficients import keller_jordan, polar_express  # noqa: F401
@@ -26,4 +27,6 @@ __all__ = [
     "muon_nonfinite", "muon_row_pass", "muon_step_noalloc", "muon_workspace_size", "muon_workspace_update", "optimizer_step", "lib",
     "ActCheckpoint", "act_pack", "act_unpack", "act_weight_grad", "act_weight_grad_workspace_size", "embedding_backward",
     "embedding_forward", "embedding_workspace_size", "layernorm_backward", "layernorm_forward", "layernorm_workspace_size",
+    "Mx4Matrix", "mx4_matmul", "mx4_matmul_workspace_size", "mx4_pack", "mx4_unpack", "rmsnorm_backward", "rmsnorm_forward",
+    "rmsnorm_workspace_size",
 ]

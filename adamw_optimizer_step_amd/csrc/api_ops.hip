@@ -1,11 +1,12 @@
-// C ABI of the operators around the optimizer step (embedding, layer norm,
-// 8-bit activation checkpoints, weight gradient): argument validation and the
-// launches. See include/muon_adamw.h for the contract of every entry point.
+// C ABI of the operators around the optimizer step (embedding, norms, 8-bit
+// activation checkpoints, weight gradient, 4-bit matrices and their product):
+// argument validation and the launches. See include/muon_adamw.h for the contract of every entry point.
 #include <algorithm>
 #include <cmath>
 
 #include "../../include/muon_adamw.h"
 #include "host.hpp"
+#include "mx4.hpp"
 #include "rows.hpp"
 #include "train_ops.hpp"
 
@@ -225,6 +226,83 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
   return done(launch_norm_bwd(a, held ? DT_ACT8 : x_dtype, dy_dtype, dx_dtype, s), fn);
 }
 
+int ma_rmsnorm_forward(const void* x, int32_t x_dtype, const void* residual, int32_t residual_dtype, int64_t rows, int64_t cols,
+                       const float* gain, float eps, void* total, void* y, int32_t y_dtype, float* rstd, uint8_t* held_q,
+                       uint8_t* held_scale, void* stream) {
+  const char* fn = "ma_rmsnorm_forward";
+  EntryMark mark(fn);
+  int rc;
+  if ((rc = check_matrix(fn, rows, 0, kMaxRows, cols, kMaxNormCols)) || (rc = check_dtype(fn, "x", x_dtype))) return rc;
+  if (residual && (rc = check_dtype(fn, "residual", residual_dtype))) return rc;
+  if (!std::isfinite(eps) || eps < 0.0f) return fail(MA_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if (!held_q != !held_scale) return fail(MA_ERR_INVALID_ARG, "%s: a checkpoint needs both q and scale", fn);
+  if (rows > 0 && !residual != !total) return fail(MA_ERR_INVALID_ARG, "%s: total and residual are given together", fn);
+  if ((y || !held_q) && (rc = check_dtype(fn, "y", y_dtype))) return rc;
+  const int t_dtype = residual ? residual_dtype : x_dtype;
+  const int64_t pitch = act_pitch(cols), t_bytes = rows * cols * dt_size(t_dtype);
+  const Buf bufs[] = {{x, rows * cols * dt_size(x_dtype), (int)dt_size(x_dtype), false, false, "x"},
+                      {residual, t_bytes, (int)dt_size(t_dtype), false, true, "residual"},
+                      {gain, cols * 4, 4, false, true, "gain"},
+                      {total, t_bytes, (int)dt_size(t_dtype), true, true, "total"},
+                      {y, y ? rows * cols * dt_size(y_dtype) : rows, y ? (int)dt_size(y_dtype) : 1, true, held_q != nullptr, "y"},
+                      {rstd, rows * 4, 4, true, false, "rstd"},
+                      {held_q, rows * pitch, 16, true, true, "the checkpoint's q"},
+                      {held_scale, rows * (pitch / kActBlock), 1, true, true, "the checkpoint's scale"}};
+  if ((rc = check_buffers(fn, bufs))) return rc;
+  if (rows == 0) return MA_OK;
+  if ((rc = check_stream_device(stream, "the stream"))) return rc;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const RmsFwdArgs a{x, residual, gain, total, y, rstd, held_q, held_scale, rows, (int32_t)cols, eps};
+  ProfScope ps(MA_K_RMSNORM, s);
+  return done(launch_rms_fwd(a, x_dtype, t_dtype, y ? y_dtype : MA_BF16, s), fn);
+}
+
+static size_t rms_workspace(int64_t rows, int64_t cols) {
+  return norm_bwd_direct(rows) ? 0 : (size_t)round_up(norm_bwd_blocks(rows, cols) * round_up(cols, 32) * 4, MA_WORKSPACE_ALIGN);
+}
+
+size_t ma_rmsnorm_workspace_size(int64_t rows, int64_t cols) {
+  if (check_matrix("ma_rmsnorm_workspace_size", rows, 0, kMaxRows, cols, kMaxNormCols)) return 0;
+  return rms_workspace(rows, cols);
+}
+
+int ma_rmsnorm_backward(const void* dy, int32_t dy_dtype, const void* t, int32_t t_dtype, const uint8_t* held_q, const uint8_t* held_scale,
+                        int64_t rows, int64_t cols, const float* rstd, const float* gain, const void* dtotal, void* dx, int32_t dx_dtype,
+                        float* dgain, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "ma_rmsnorm_backward";
+  EntryMark mark(fn);
+  int rc;
+  if ((rc = check_matrix(fn, rows, 0, kMaxRows, cols, kMaxNormCols)) || (rc = check_dtype(fn, "dy", dy_dtype)) ||
+      (rc = check_dtype(fn, "dx", dx_dtype)) || (rc = check_flag(fn, accumulate)))
+    return rc;
+  if (!held_q != !held_scale) return fail(MA_ERR_INVALID_ARG, "%s: a checkpoint needs both q and scale", fn);
+  if (t && held_q) return fail(MA_ERR_INVALID_ARG, "%s: give t or its checkpoint, not both", fn);
+  const bool held = !t;   // (an empty t may be null too)
+  if (!held && (rc = check_dtype(fn, "t", t_dtype))) return rc;
+  if (rows > 0 && dx_dtype != (held ? dy_dtype : t_dtype))
+    return fail(MA_ERR_UNSUPPORTED, "%s: dx has the type of t, or of dy where t is a checkpoint", fn);
+  const int64_t pitch = act_pitch(cols), dx_bytes = rows * cols * dt_size(dx_dtype);
+  const size_t need = dgain ? rms_workspace(rows, cols) : 0;
+  const Buf bufs[] = {{dy, rows * cols * dt_size(dy_dtype), (int)dt_size(dy_dtype), false, false, "dy"},
+                      {t, held ? 0 : rows * cols * dt_size(t_dtype), held ? 1 : (int)dt_size(t_dtype), false, false, "t"},
+                      {held_q, rows * pitch, 16, false, !held, "t and the checkpoint's q"},
+                      {held_scale, rows * (pitch / kActBlock), 1, false, !held, "the checkpoint's scale"},
+                      {rstd, rows * 4, 4, false, false, "rstd"},
+                      {gain, cols * 4, 4, false, true, "gain"},
+                      {dtotal, dx_bytes, (int)dt_size(dx_dtype), false, true, "dtotal"},
+                      {dx, dx_bytes, (int)dt_size(dx_dtype), true, false, "dx"},
+                      {dgain, cols * 4, 4, true, true, "dgain"},
+                      {workspace, (int64_t)need, 1, true, true, "the workspace"}};
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, need)) || (rc = check_buffers(fn, bufs))) return rc;
+  if (rows == 0 && (!dgain || accumulate)) return MA_OK;
+  if ((rc = check_stream_device(stream, "the stream"))) return rc;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const RmsBwdArgs a{dy, t, held_q, held_scale, rstd, gain, dtotal, dx, dgain, need ? reinterpret_cast<float*>(workspace) : nullptr,
+                     rows, (int32_t)cols, accumulate, norm_bwd_blocks(rows, cols)};
+  ProfScope ps(MA_K_RMSNORM, s);
+  return done(launch_rms_bwd(a, held ? DT_ACT8 : t_dtype, dy_dtype, dx_dtype, s), fn);
+}
+
 static int act_call(const char* fn, const void* x, int32_t dtype, bool pack, int64_t rows, int64_t cols, const uint8_t* q, const uint8_t* scale,
                     void* stream) {
   EntryMark mark(fn);
@@ -250,6 +328,81 @@ int ma_act_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, uint
 
 int ma_act_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, void* out, int32_t out_dtype, void* stream) {
   return act_call("ma_act_unpack", out, out_dtype, false, rows, cols, q, scale, stream);
+}
+
+// bytes of q and of scale of a 4-bit rows x cols matrix
+static int64_t mx4_q_bytes(int64_t rows, int64_t cols) { return rows * mx4_tiles(cols) * (kMx4Tile / 2); }
+static int64_t mx4_scale_bytes(int64_t rows, int64_t cols) { return rows * mx4_tiles(cols) * 4; }
+
+static int mx4_call(const char* fn, const void* x, int32_t dtype, bool pack, int64_t rows, int64_t cols, int32_t transpose, const uint8_t* q,
+                    const uint8_t* scale, void* stream) {
+  EntryMark mark(fn);
+  int rc;
+  if ((rc = check_matrix(fn, rows, 0, kMaxRows, cols, kMaxCols)) || (rc = check_dtype(fn, pack ? "x" : "out", dtype))) return rc;
+  if (transpose != 0 && transpose != 1) return fail(MA_ERR_INVALID_ARG, "%s: transpose %d is not 0 or 1", fn, transpose);
+  // the packed matrix's sizes
+  const int64_t pr = transpose ? cols : rows, pc = transpose ? rows : cols;
+  if (pr * mx4_tiles(pc) * kMx4Tile > (dtype == MA_F32 ? kMaxElems / 2 : kMaxElems))
+    return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements (2^35 fp32 ones)", fn);
+  const Buf bufs[] = {{x, rows * cols * dt_size(dtype), (int)dt_size(dtype), !pack, false, pack ? "x" : "out"},
+                      {q, mx4_q_bytes(pr, pc), 16, pack, false, "q"},
+                      {scale, mx4_scale_bytes(pr, pc), 4, pack, false, "scale"}};
+  if ((rc = check_buffers(fn, bufs))) return rc;
+  if (rows == 0) return MA_OK;
+  if ((rc = check_stream_device(stream, "the stream"))) return rc;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const Mx4Args a{pack ? x : nullptr, pack ? nullptr : const_cast<void*>(x), const_cast<uint8_t*>(q), const_cast<uint8_t*>(scale), rows, (int32_t)cols};
+  ProfScope ps(MA_K_MX4, s);
+  return done(pack ? launch_mx4_pack(a, dtype, transpose != 0, s) : launch_mx4_unpack(a, dtype, s), fn);
+}
+
+int ma_mx4_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int32_t transpose, uint8_t* q, uint8_t* scale, void* stream) {
+  return mx4_call("ma_mx4_pack", x, x_dtype, true, rows, cols, transpose, q, scale, stream);
+}
+
+int ma_mx4_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, void* out, int32_t out_dtype, void* stream) {
+  return mx4_call("ma_mx4_unpack", out, out_dtype, false, rows, cols, 0, q, scale, stream);
+}
+
+static int mx4_matmul_sizes(const char* fn, int64_t rows, int64_t outs, int64_t ins, int32_t x_bits) {
+  int rc;
+  if ((rc = check_size(fn, "rows", rows, 0, kMaxRows)) || (rc = check_size(fn, "outs", outs, 1, kMaxCols / 2)) ||
+      (rc = check_size(fn, "ins", ins, 1, kMaxCols / 2)))
+    return rc;
+  if (x_bits != 4 && x_bits != 8) return fail(MA_ERR_UNSUPPORTED, "%s: x_bits %d is neither 4 nor 8", fn, x_bits);
+  const int64_t pitch = mx4_tiles(ins) * kMx4Tile;
+  if (rows * outs > kMaxElems / 8) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^33 outputs", fn);
+  if (rows * pitch > kMaxElems || outs * pitch > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
+  return MA_OK;
+}
+
+size_t ma_mx4_matmul_workspace_size(int64_t rows, int64_t outs, int64_t ins, int32_t x_bits) {
+  if (mx4_matmul_sizes("ma_mx4_matmul_workspace_size", rows, outs, ins, x_bits)) return 0;
+  return 0;
+}
+
+int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int64_t rows, const uint8_t* wq, const uint8_t* wscale,
+                  int64_t outs, int64_t ins, void* y, int32_t y_dtype, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  const char* fn = "ma_mx4_matmul";
+  EntryMark mark(fn);
+  int rc;
+  if ((rc = mx4_matmul_sizes(fn, rows, outs, ins, x_bits)) || (rc = check_dtype(fn, "y", y_dtype)) || (rc = check_flag(fn, accumulate))) return rc;
+  const size_t need = 0;
+  const int64_t tiles = mx4_tiles(ins);
+  const Buf bufs[] = {{xq, rows * tiles * (x_bits == 8 ? 128 : 64), 16, false, false, "xq"},
+                      {xscale, rows * tiles * (x_bits == 8 ? 1 : 4), x_bits == 8 ? 1 : 4, false, false, "xscale"},
+                      {wq, mx4_q_bytes(outs, ins), 16, false, false, "wq"},
+                      {wscale, mx4_scale_bytes(outs, ins), 4, false, false, "wscale"},
+                      {y, rows * outs * dt_size(y_dtype), (int)dt_size(y_dtype), true, false, "y"},
+                      {workspace, (int64_t)need, 1, true, true, "the workspace"}};
+  if ((rc = check_workspace(fn, workspace, workspace_bytes, need)) || (rc = check_buffers(fn, bufs))) return rc;
+  if (rows == 0) return MA_OK;
+  if ((rc = check_stream_device(stream, "the stream"))) return rc;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const Mx4MatmulArgs a{xq, xscale, wq, wscale, y, rows, (int32_t)outs, (int32_t)ins, accumulate};
+  ProfScope ps(MA_K_MX4_MATMUL, s);
+  return done(launch_mx4_matmul(a, x_bits, y_dtype, s), fn);
 }
 
 static int wgrad_sizes(const char* fn, int64_t tokens, int64_t outs, int64_t ins, int32_t dy_dtype) {

@@ -1,5 +1,6 @@
 // Launch descriptors of the operators around the optimizer step: embedding,
-// layer norm, 8-bit activation checkpoints and the weight gradient.
+// the norms, 8-bit activation checkpoints, 4-bit matrices and their product, and the
+// weight gradient.
 #pragma once
 #include "common.hpp"
 
@@ -77,6 +78,37 @@ struct NormBwdArgs {
 int norm_bwd_blocks(int64_t rows, int64_t cols);
 bool norm_bwd_direct(int64_t rows);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dt, int dy_dt, int dx_dt, hipStream_t s);
+// out (+)= the sums of `blocks` rows of partial sums, [cols / 32][blocks][32]
+hipError_t launch_norm_cols(const float* partial, int blocks, int cols, int accumulate, float* out, hipStream_t s);
+
+// ---- root-mean-square norm ----
+struct RmsFwdArgs {
+  const void* x;
+  const void* residual;       // may be null; else `total` receives x + residual
+  const float* gain;          // may be null
+  void* total;                // the residual's type
+  void* y;                    // may be null where q is there
+  float* rstd;                // 1 per row: 1 / sqrt(mean of squares + eps)
+  uint8_t *q, *qscale;        // y in 8 bits, or null
+  int64_t rows;
+  int32_t cols;
+  float eps;
+};
+hipError_t launch_rms_fwd(const RmsFwdArgs& a, int x_dt, int total_dt, int y_dt, hipStream_t s);
+
+struct RmsBwdArgs {
+  const void* dy;
+  const void* x;              // the rows that were normalised, or q / qscale
+  const uint8_t *q, *qscale;
+  const float *rstd, *gain;
+  const void* dtotal;         // may be null; dx's type
+  void* dx;
+  float* dgain;               // may be null
+  float* partial;             // [cols / 32][blocks][32]; null if not kept
+  int64_t rows;
+  int32_t cols, accumulate, blocks;
+};
+hipError_t launch_rms_bwd(const RmsBwdArgs& a, int x_dt, int dy_dt, int dx_dt, hipStream_t s);
 
 // ---- 8-bit activation checkpoints ----
 struct ActArgs {
@@ -88,6 +120,26 @@ struct ActArgs {
 };
 hipError_t launch_act_pack(const ActArgs& a, int x_dt, hipStream_t s);
 hipError_t launch_act_unpack(const ActArgs& a, int out_dt, hipStream_t s);
+
+// ---- 4-bit matrices ----
+struct Mx4Args {
+  const void* x;              // rows x cols, packed as they are or transposed
+  void* out;
+  uint8_t *q, *scale;
+  int64_t rows;
+  int32_t cols;
+};
+hipError_t launch_mx4_pack(const Mx4Args& a, int x_dt, bool transpose, hipStream_t s);
+hipError_t launch_mx4_unpack(const Mx4Args& a, int out_dt, hipStream_t s);
+
+struct Mx4MatmulArgs {
+  const uint8_t *xq, *xscale;   // rows x ins, in 4 bits or 8
+  const uint8_t *wq, *wscale;   // outs x ins, in 4 bits
+  void* y;                      // rows x outs
+  int64_t rows;
+  int32_t outs, ins, accumulate;
+};
+hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int x_bits, int y_dt, hipStream_t s);
 
 // ---- weight gradient out of a checkpoint ----
 struct WgradArgs {

@@ -1,5 +1,6 @@
-"""Python binding of the operators around the optimizer step: embedding, layer
-norm, 8-bit activation checkpoints and the weight gradient that reads one.
+"""Python binding of the operators around the optimizer step: embedding, norms,
+8-bit activation checkpoints and the weight gradient that reads one, 4-bit
+matrices and the product that reads them.
 
 They fill the gradient buffers that ``adamw_step``, ``lion_step`` and
 ``muon_step`` read. As in ``api``, this is argument marshalling only: every
@@ -344,6 +345,250 @@ def layernorm_backward(dy: torch.Tensor, x: Union[torch.Tensor, ActCheckpoint], 
                                           _ptr(gain), dx.data_ptr(), _dt(dx), _ptr(dgain), _ptr(dbias), int(bool(accumulate)),
                                           _ptr(ws), ws.numel() if ws is not None else 0, _current_stream(dev)))
     return dx
+
+
+# ---------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------
+def rmsnorm_forward(x: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                    dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+                    rstd: Optional[torch.Tensor] = None, held: Optional[ActCheckpoint] = None,
+                    stream=None) -> Tuple[Union[torch.Tensor, ActCheckpoint], torch.Tensor, torch.Tensor]:
+    """Root-mean-square norm over the last dimension of ``x + residual``; ``gain``
+    is fp32 ``[cols]``. Returns ``(y, total, rstd)``: ``y`` in ``dtype`` (x's by
+    default), the sum in the residual's type (``x`` itself without a residual),
+    which is what is normalised, and fp32 ``[rows]`` reciprocal roots; the
+    backward pass reads the last two. With ``held``
+    (``ActCheckpoint.empty(rows, cols, device)``) y goes there, in 8 bits, and is
+    returned so; with ``out`` as well it goes to both and ``out`` is returned
+    (``ma_rmsnorm_forward``)."""
+    _check("x", x, _DT)
+    rows, cols = _rows("x", x)
+    _param("gain", gain, cols)
+    if residual is not None:
+        _check("residual", residual, _DT, x.shape)
+    if out is not None:
+        _check("out", out, (dtype,) if dtype is not None else _DT, x.shape)
+    elif dtype is not None and held is not None:
+        raise ValueError("dtype is that of out: with held alone y has none")
+    elif dtype is not None and dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    if total is not None:
+        if residual is None:
+            raise ValueError("total: there is no residual to add")
+        _check("total", total, (residual.dtype,), x.shape)
+    if rstd is not None:
+        _check("rstd", rstd, (torch.float32,), (rows,))
+    kept = () if held is None else _check_checkpoint("held", held, rows, cols)._tensors
+    dev = _device(x, gain, residual, out, total, rstd, *kept)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: rmsnorm_forward(x, gain, residual, eps, dtype, out, total, rstd, held))
+    if out is None and held is None:
+        out = torch.empty_like(x) if dtype is None or dtype == x.dtype else x.new_empty(x.shape, dtype=dtype)
+    if total is None and residual is not None:
+        total = torch.empty_like(residual)
+    if rstd is None:
+        rstd = x.new_empty((rows,), dtype=torch.float32)
+    q, sc = held._pointers() if held is not None else (None, None)
+    L.check(L.lib().ma_rmsnorm_forward(x.data_ptr(), _dt(x), _ptr(residual), 0 if residual is None else _dt(residual), rows, cols,
+                                       _ptr(gain), eps, _ptr(total), _ptr(out), 0 if out is None else _dt(out), rstd.data_ptr(), q, sc,
+                                       _current_stream(dev)))
+    return held if out is None else out, x if total is None else total, rstd
+
+
+def rmsnorm_workspace_size(rows: int, cols: int) -> int:
+    """Bytes of workspace (0: none needed) for at most ``rows`` rows."""
+    n = L.lib().ma_rmsnorm_workspace_size(rows, cols)
+    if n == 0 and not (0 <= rows <= 1 << 24 and 1 <= cols <= 16384 and rows * cols <= 1 << 36):
+        L.check(L.MA_ERR_INVALID_ARG)
+    return int(n)
+
+
+def rmsnorm_backward(dy: torch.Tensor, total: Union[torch.Tensor, ActCheckpoint], rstd: torch.Tensor,
+                     gain: Optional[torch.Tensor] = None, dtotal: Optional[torch.Tensor] = None,
+                     dgain: Optional[torch.Tensor] = None, accumulate: bool = False, dx: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The backward pass of ``rmsnorm_forward`` from ``dy``, ``rstd`` and what it
+    normalised, ``total`` or that as an 8-bit checkpoint. ``dtotal`` is the
+    gradient that reaches ``total`` on other ways. Returns ``dx`` (total's type;
+    dy's for a checkpoint; dtotal has the same), the gradient of ``x`` and of
+    ``residual`` alike. The gain's gradient goes to the fp32 ``[cols]`` buffer
+    ``dgain`` where given, written or, with ``accumulate``, added to
+    (``ma_rmsnorm_backward``)."""
+    _check("dy", dy, _DT)
+    rows, cols = _rows("dy", dy)
+    if isinstance(total, ActCheckpoint):
+        _check_checkpoint("total", total, rows, cols)
+        t, held, dx_dtype, td = None, total._tensors, dy.dtype, 0
+    else:
+        _check("total", total, _DT, dy.shape)
+        t, held, dx_dtype, td = total, (), total.dtype, _dt(total)
+    _check("rstd", rstd, (torch.float32,), (rows,))
+    _param("gain", gain, cols)
+    _param("dgain", dgain, cols)
+    if dtotal is not None:
+        _check("dtotal", dtotal, (dx_dtype,), dy.shape)
+    if dx is not None:
+        _check("dx", dx, (dx_dtype,), dy.shape)
+    _check_workspace(workspace)
+    dev = _device(dy, t, *held, rstd, gain, dtotal, dgain, dx, workspace)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: rmsnorm_backward(dy, total, rstd, gain, dtotal, dgain, accumulate, dx, workspace))
+    if dx is None:
+        dx = torch.empty_like(dy if t is None else t)
+    q, sc = total._pointers() if held else (None, None)
+    need = rmsnorm_workspace_size(rows, cols) if dgain is not None else 0
+    ws = _workspace(workspace, need, dy) if need or workspace is not None else None
+    L.check(L.lib().ma_rmsnorm_backward(dy.data_ptr(), _dt(dy), _ptr(t), td, q, sc, rows, cols, rstd.data_ptr(), _ptr(gain),
+                                        _ptr(dtotal), dx.data_ptr(), _dt(dx), _ptr(dgain), int(bool(accumulate)),
+                                        _ptr(ws), ws.numel() if ws is not None else 0, _current_stream(dev)))
+    return dx
+
+
+# ---------------------------------------------------------------------------
+# 4-bit matrices and their product
+# ---------------------------------------------------------------------------
+class Mx4Matrix:
+    """A matrix ``[rows, cols]`` held in 4 bits: ``q`` (uint8 ``[rows, P / 2]``,
+    P = cols rounded up to a multiple of 128; the even column in a byte's lower
+    half) and ``scale`` (uint8 ``[P / 128, rows, 4]``: for each 128 columns and
+    row the powers of two of its 4 blocks of 32), as ``mx4_pack`` writes them.
+    ``empty`` keeps both in one allocation."""
+
+    __slots__ = ("rows", "cols", "_tensors")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int):
+        if cols < 1:
+            raise ValueError("a 4-bit matrix has at least one column")
+        tiles = -(-int(cols) // L.MA_MX4_TILE)
+        rows = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 2 else -1
+        _check("q", q, (torch.uint8,), (rows, tiles * (L.MA_MX4_TILE // 2)))
+        _check("scale", scale, (torch.uint8,), (tiles, rows, 4))
+        self._tensors = (q, scale)
+        self.rows, self.cols = rows, int(cols)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device) -> "Mx4Matrix":
+        """Room for a ``[rows, cols]`` matrix."""
+        if rows < 0 or cols < 1:
+            raise ValueError(f"no 4-bit matrix of {rows} rows and {cols} columns")
+        self = cls.__new__(cls)
+        self.rows, self.cols = rows, cols
+        self._tensors = (torch.empty(self.nbytes(), dtype=torch.uint8, device=device),)
+        return self
+
+    def _q_bytes(self) -> int:
+        return self.rows * (-(-self.cols // L.MA_MX4_TILE)) * (L.MA_MX4_TILE // 2)
+
+    @property
+    def q(self) -> torch.Tensor:
+        t = self._tensors
+        return t[0] if len(t) == 2 else t[0][:self._q_bytes()].view(self.rows, -(-self.cols // L.MA_MX4_TILE) * (L.MA_MX4_TILE // 2))
+
+    @property
+    def scale(self) -> torch.Tensor:
+        t = self._tensors
+        return t[1] if len(t) == 2 else t[0][self._q_bytes():].view(-(-self.cols // L.MA_MX4_TILE), self.rows, 4)
+
+    def nbytes(self) -> int:
+        return self.rows * (-(-self.cols // L.MA_MX4_TILE)) * (L.MA_MX4_TILE // 2 + L.MA_MX4_TILE // L.MA_MX4_BLOCK)
+
+    def _pointers(self) -> Tuple[int, int]:
+        t = self._tensors
+        p = t[0].data_ptr()
+        return p, t[1].data_ptr() if len(t) == 2 else p + self._q_bytes()
+
+
+def mx4_pack(x: torch.Tensor, transpose: bool = False, out: Optional[Mx4Matrix] = None, stream=None) -> Mx4Matrix:
+    """``x`` (its last dimension the columns, the others flattened to rows) in 4
+    bits; with ``transpose`` its transpose, ``[cols, rows]``, whose blocks of 32
+    go along x's rows (``ma_mx4_pack``)."""
+    _check("x", x, _DT)
+    rows, cols = _rows("x", x)
+    if transpose and rows == 0:
+        raise ValueError("x has no rows: its transpose would have no columns")
+    shape = (cols, rows) if transpose else (rows, cols)
+    if out is not None:
+        if not isinstance(out, Mx4Matrix):
+            raise TypeError(f"out: expected an Mx4Matrix, got {type(out).__name__}")
+        if (out.rows, out.cols) != shape:
+            raise ValueError(f"out: a 4-bit matrix of {(out.rows, out.cols)}, expected {shape}")
+    dev = _device(x, *out._tensors) if out is not None else _device(x)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: mx4_pack(x, transpose, out))
+    if out is None:
+        out = Mx4Matrix.empty(*shape, x.device)
+    L.check(L.lib().ma_mx4_pack(x.data_ptr(), _dt(x), rows, cols, int(bool(transpose)), *out._pointers(), _current_stream(dev)))
+    return out
+
+
+def mx4_unpack(matrix: Mx4Matrix, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """The values a 4-bit matrix holds as ``[rows, cols]`` in ``dtype`` (exact in
+    bf16 and fp32 alike; ``ma_mx4_unpack``)."""
+    if not isinstance(matrix, Mx4Matrix):
+        raise TypeError(f"expected an Mx4Matrix, got {type(matrix).__name__}")
+    rows, cols = matrix.rows, matrix.cols
+    if out is not None:
+        _check("out", out, _DT)
+        if out.dim() < 1 or out.shape[-1] != cols or out.numel() != rows * cols:
+            raise ValueError(f"out: expected {rows} rows of {cols} columns, got {tuple(out.shape)}")
+    elif dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    dev = _device(*matrix._tensors, out)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: mx4_unpack(matrix, dtype, out))
+    if out is None:
+        out = matrix._tensors[0].new_empty((rows, cols), dtype=dtype)
+    L.check(L.lib().ma_mx4_unpack(*matrix._pointers(), rows, cols, out.data_ptr(), _dt(out), _current_stream(dev)))
+    return out
+
+
+def mx4_matmul_workspace_size(rows: int, outs: int, ins: int, x_bits: int = 4) -> int:
+    """Bytes of workspace (0: none needed) for exactly these sizes, and rows held
+    in ``x_bits`` (4 or 8) bits: fewer rows can need more."""
+    n = L.lib().ma_mx4_matmul_workspace_size(rows, outs, ins, x_bits)
+    if n == 0:
+        pitch = -(-ins // L.MA_MX4_TILE) * L.MA_MX4_TILE
+        if x_bits not in (4, 8):
+            L.check(L.MA_ERR_UNSUPPORTED)
+        if not (0 <= rows <= 1 << 24 and 1 <= outs <= 1 << 23 and 1 <= ins <= 1 << 23 and max(rows * outs, rows * pitch, outs * pitch) <= 1 << 36):
+            L.check(L.MA_ERR_INVALID_ARG)
+    return int(n)
+
+
+def mx4_matmul(x: Union[Mx4Matrix, ActCheckpoint], w: Mx4Matrix, dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+               accumulate: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A linear layer on held values: ``x w^T`` as ``[rows, outs]`` in ``dtype``
+    (bf16 by default), of ``x`` ``[rows, ins]`` in 4 bits or as an 8-bit
+    checkpoint and the 4-bit weights ``w`` ``[outs, ins]``. With ``accumulate`` the
+    product is added to ``out`` (``ma_mx4_matmul``)."""
+    if not isinstance(x, (Mx4Matrix, ActCheckpoint)):
+        raise TypeError(f"x: expected an Mx4Matrix or an ActCheckpoint, got {type(x).__name__}")
+    if not isinstance(w, Mx4Matrix):
+        raise TypeError(f"w: expected an Mx4Matrix, got {type(w).__name__}")
+    rows, outs, ins, bits = x.rows, w.rows, w.cols, 8 if isinstance(x, ActCheckpoint) else 4
+    if x.cols != ins:
+        raise ValueError(f"x has {x.cols} columns, w {ins}")
+    if out is not None:
+        _check("out", out, (dtype,) if dtype is not None else _DT)
+        if out.dim() < 1 or out.shape[-1] != outs or out.numel() != rows * outs:
+            raise ValueError(f"out: expected {rows} rows of {outs} columns, got {tuple(out.shape)}")
+    elif accumulate:
+        raise ValueError("accumulate: there is no out to add to")
+    elif dtype is not None and dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+    _check_workspace(workspace)
+    dev = _device(*x._tensors, *w._tensors, out, workspace)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, lambda: mx4_matmul(x, w, dtype, out, accumulate, workspace))
+    if out is None:
+        out = w._tensors[0].new_empty((rows, outs), dtype=dtype or torch.bfloat16)
+    need = mx4_matmul_workspace_size(rows, outs, ins, bits)
+    ws = _workspace(workspace, need, out) if need or workspace is not None else None
+    L.check(L.lib().ma_mx4_matmul(*x._pointers(), bits, rows, *w._pointers(), outs, ins, out.data_ptr(), _dt(out), int(bool(accumulate)),
+                                  _ptr(ws), ws.numel() if ws is not None else 0, _current_stream(dev)))
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -403,6 +403,36 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
                           void* dx, int32_t dx_dtype, float* dgain, float* dbias, int32_t accumulate, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* Root-mean-square norm with the residual's addition, per row (rows <= 2^24,
+ * cols <= 16384, rows * cols <= 2^36):
+ *   t = x + residual, rounded to the residual's type, written to `total`;
+ *       without a residual t = x, and `total` must be null
+ *   rstd = 1 / sqrt(sum t^2 / cols + eps)
+ *   y = t * rstd * gain                        gain: cols fp32 values, may be null
+ * The norm reads t as it is stored. rstd (rows fp32) and t are what the backward
+ * pass reads. y may be null where held_q and held_scale (both or neither) are
+ * given: they receive y as an 8-bit checkpoint (ma_act_pack), rounded from fp32
+ * once; with y given too, both are written. Sums are fp32: a row whose sum of
+ * squares passes its range has rstd 0; a row of zeros with eps 0 has y NaN. */
+int ma_rmsnorm_forward(const void* x, int32_t x_dtype, const void* residual, int32_t residual_dtype, int64_t rows, int64_t cols,
+                       const float* gain, float eps, void* total, void* y, int32_t y_dtype, float* rstd, uint8_t* held_q,
+                       uint8_t* held_scale, void* stream);
+
+/* Its backward pass from dy, rstd and either t or t's 8-bit checkpoint (the other
+ * null): with xh = t * rstd and g = dy * gain (gain may be null),
+ *   dx = dtotal + rstd * (g - xh * mean(g * xh));  dgain (+)= sum over rows of dy * xh
+ * dtotal is the gradient that reaches t on other ways (the residual stream's; may
+ * be null), so dx is the gradient of x and of the residual alike. dx and dtotal
+ * have t's type, or dy's where t is held in 8 bits. dgain (cols fp32 values) may be
+ * null; else at least ma_rmsnorm_workspace_size bytes of workspace are needed, which
+ * may be 0 (few rows); that of more rows serves fewer too. accumulate applies to
+ * dgain. */
+size_t ma_rmsnorm_workspace_size(int64_t rows, int64_t cols);
+int ma_rmsnorm_backward(const void* dy, int32_t dy_dtype, const void* t, int32_t t_dtype, const uint8_t* held_q,
+                        const uint8_t* held_scale, int64_t rows, int64_t cols, const float* rstd, const float* gain,
+                        const void* dtotal, void* dx, int32_t dx_dtype, float* dgain, int32_t accumulate, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 /* 8-bit activation checkpoints. q (rows x P bytes, P = cols rounded up to a
  * multiple of MA_ACT_BLOCK, 16-byte aligned, zero beyond cols) holds e4m3 (OCP)
  * values, scale (rows x P / MA_ACT_BLOCK bytes) a power of two for each block of
@@ -437,6 +467,42 @@ int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const
                        int64_t outs, int64_t ins, void* grad, int32_t grad_dtype, int32_t accumulate, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* 4-bit matrices: blocks of MA_MX4_BLOCK columns of a row with one power of two
+ * each, and e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives). With
+ * P = cols rounded up to a multiple of MA_MX4_TILE:
+ *   q      rows x P/2 bytes, 16-byte aligned; two values a byte, the even column in
+ *          the lower half; zero beyond cols
+ *   scale  P/MA_MX4_TILE x rows x 4 bytes, 4-byte aligned: for every tile of columns
+ *          and row the bytes of its 4 blocks; the byte s stands for 2^(s - 127), 255
+ *          for NaN (E8M0)
+ * Packing takes the least exponent e in -126..125 for which the block's largest
+ * magnitude over 2^e rounds to at most 6, and rounds x / 2^e to nearest even: every
+ * value is off by half a step at most (|x| / 5 from 2^e up, 2^e / 4 below). At
+ * e = 125 values stop at 6 * 2^125. A block with a NaN or an infinity is held as NaN.
+ * Every held value is exact in bf16. transpose = 1 packs x^T: q and scale then
+ * describe a cols x rows matrix, whose blocks go along x's rows. Unpacking rounds
+ * nothing, whatever the scale bytes. Limits: rows, cols <= 2^24, and padded rows of
+ * at most 2^36 values in all (2^35 where x or out is fp32). */
+#define MA_MX4_BLOCK 32
+#define MA_MX4_TILE 128
+int ma_mx4_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int32_t transpose, uint8_t* q, uint8_t* scale,
+                void* stream);
+int ma_mx4_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, void* out, int32_t out_dtype,
+                  void* stream);
+
+/* A linear layer on held values: y[m,n] (+)= sum over k of x[m,k] * w[n,k].
+ * wq, wscale: a 4-bit outs x ins matrix; xq, xscale: rows x ins held in 4 bits
+ * (x_bits 4) or as an 8-bit checkpoint (x_bits 8). The held values are multiplied as
+ * they are; sums are fp32, y (rows x outs) is rounded once. A NaN that is held
+ * reaches every output of its row (of w: of its column).
+ * Limits: rows <= 2^24, outs, ins <= 2^23, rows * outs <= 2^33, rows * P and outs * P
+ * <= 2^36 (P = ins rounded up to a multiple of MA_MX4_TILE). workspace: at least ma_mx4_matmul_workspace_size
+ * bytes, which may be 0; that is the need of exactly these sizes. */
+size_t ma_mx4_matmul_workspace_size(int64_t rows, int64_t outs, int64_t ins, int32_t x_bits);
+int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int64_t rows, const uint8_t* wq,
+                  const uint8_t* wscale, int64_t outs, int64_t ins, void* y, int32_t y_dtype, int32_t accumulate,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Status text for a code, and the calling thread's last error message. */
 const char* ma_status_string(int status);
 const char* ma_last_error(void);
@@ -468,7 +534,10 @@ typedef enum {
   MA_K_LAYERNORM = 11,  /* one ma_layernorm_* call */
   MA_K_ACT = 12,        /* ma_act_pack, ma_act_unpack */
   MA_K_WEIGHT_GRAD = 13, /* one ma_act_weight_grad call */
-  MA_K_COUNT = 14
+  MA_K_RMSNORM = 14,    /* one ma_rmsnorm_* call */
+  MA_K_MX4 = 15,        /* ma_mx4_pack, ma_mx4_unpack */
+  MA_K_MX4_MATMUL = 16, /* one ma_mx4_matmul call */
+  MA_K_COUNT = 17
 } ma_kernel_kind;
 
 int ma_profile_begin(int32_t max_launches);

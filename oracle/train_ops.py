@@ -1,5 +1,6 @@
 """The operators around the optimizer step in fp64, from their formulas:
-embedding, layer norm, 8-bit activation checkpoints, the weight gradient."""
+embedding, norms, 8-bit activation checkpoints, the weight gradient, 4-bit
+matrices and their product."""
 import numpy as np
 
 ACT_BLOCK = 128
@@ -102,3 +103,80 @@ def act_weight_grad(dy, x, grad=None):
     dy, x = np.asarray(dy, np.float64), np.asarray(x, np.float64)
     out = dy.T @ x
     return (out if grad is None else out + np.asarray(grad, np.float64)), np.abs(dy).T @ np.abs(x)
+
+
+def bf16_nearest(v):
+    """v (fp32) rounded to bf16, to nearest even, as fp32; infinities and NaN stay."""
+    b = np.ascontiguousarray(v, np.float32).view(np.uint32).astype(np.uint64)
+    r = ((b + 0x7FFF + ((b >> 16) & 1)) & 0xFFFF0000).astype(np.uint32).view(np.float32)
+    return np.where(np.isnan(v), np.float32(np.nan), r)
+
+
+def rmsnorm_forward(x, gain=None, residual=None, eps=1e-5, bf16_stream=False):
+    """y, the normalised rows (x + residual in fp32, rounded to bf16 for a bf16
+    stream) and rstd [rows, 1]."""
+    t = np.asarray(x, np.float64)
+    if residual is not None:
+        with np.errstate(invalid="ignore", over="ignore"):
+            s = np.asarray(x, np.float32) + np.asarray(residual, np.float32)
+        t = (bf16_nearest(s) if bf16_stream else s).astype(np.float64)
+    rstd = 1.0 / np.sqrt((t * t).mean(-1, keepdims=True) + float(np.float32(eps)))
+    y = t * rstd
+    return (y if gain is None else y * np.asarray(gain, np.float64)), t, rstd
+
+
+def rmsnorm_backward(dy, t, rstd, gain=None, dtotal=None):
+    """dx and dgain for a given rstd [rows, 1]."""
+    dy, t = np.asarray(dy, np.float64), np.asarray(t, np.float64)
+    xh = t * rstd
+    g = dy if gain is None else dy * np.asarray(gain, np.float64)
+    dx = rstd * (g - xh * (g * xh).mean(-1, keepdims=True))
+    return (dx if dtotal is None else dx + np.asarray(dtotal, np.float64)), (dy * xh).sum(0)
+
+
+MX4_TILE, MX4_BLOCK = 128, 32
+MX4_EMIN, MX4_EMAX = -126, 125
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+
+def e2m1_code(v):
+    """The code 0..7 (8..15 negative) of the e2m1 value nearest to each v, ties to the even code; |v| > 6 to 6."""
+    a = np.minimum(np.abs(np.asarray(v, np.float64)), 6.0)
+    hi = np.clip(np.searchsorted(E2M1, a), 1, 7)
+    below, above = a - E2M1[hi - 1], E2M1[hi] - a
+    code = np.where((below < above) | ((below == above) & (hi % 2 == 1)), hi - 1, hi)
+    return (code | np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def mx4_pack(x):
+    """(q, scale) bytes of the 4-bit form of x [rows, cols]."""
+    x = np.asarray(x, np.float64)
+    rows, cols = x.shape
+    tiles = -(-cols // MX4_TILE)
+    v = np.zeros((rows, tiles * MX4_TILE))
+    v[:, :cols] = x
+    v = v.reshape(rows, -1, MX4_BLOCK)
+    bad = ~np.isfinite(v).all(-1)
+    v = np.where(bad[..., None], 0.0, v)
+    amax = np.abs(v).max(-1)
+    e = np.full(amax.shape, MX4_EMIN)
+    for k in range(MX4_EMIN, MX4_EMAX):            # the least exponent for which amax rounds to at most 6
+        e = np.where((e == k) & (amax >= 7.0 * 2.0 ** k), k + 1, e)
+    code = e2m1_code(v / 2.0 ** e[..., None].astype(np.float64)).reshape(rows, -1)
+    scale = np.where(bad, 255, e + 127).astype(np.uint8)
+    return code[:, ::2] | code[:, 1::2] << 4, np.ascontiguousarray(scale.reshape(rows, tiles, 4).transpose(1, 0, 2))
+
+
+def mx4_unpack(q, scale, cols):
+    q, scale = np.asarray(q), np.asarray(scale)
+    code = np.stack([q & 15, q >> 4], -1).reshape(q.shape[0], -1)
+    s = scale.transpose(1, 0, 2).reshape(q.shape[0], -1)
+    s = np.where(s == 255, np.nan, 2.0 ** (s.astype(np.float64) - 127)).repeat(MX4_BLOCK, 1)
+    return (np.where(code & 8, -E2M1[code & 7], E2M1[code & 7]) * s)[:, :cols]
+
+
+def mx4_matmul(x, w, y=None):
+    """x w^T (+ y) of held values, and the sum of the products' magnitudes."""
+    x, w = np.asarray(x, np.float64), np.asarray(w, np.float64)
+    out = x @ w.T
+    return (out if y is None else out + np.asarray(y, np.float64)), np.abs(x) @ np.abs(w).T
