@@ -371,14 +371,18 @@ static int mx4_matmul_sizes(const char* fn, int64_t rows, int64_t outs, int64_t 
     return rc;
   if (x_bits != 4 && x_bits != 8) return fail(MA_ERR_UNSUPPORTED, "%s: x_bits %d is neither 4 nor 8", fn, x_bits);
   const int64_t pitch = mx4_tiles(ins) * kMx4Tile;
-  if (rows * outs > kMaxElems / 8) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^33 outputs", fn);
-  if (rows * pitch > kMaxElems || outs * pitch > kMaxElems) return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
+  if (rows * outs > kMaxElems || rows * pitch > kMaxElems || outs * pitch > kMaxElems)
+    return fail(MA_ERR_INVALID_ARG, "%s: more than 2^36 elements", fn);
   return MA_OK;
+}
+
+static size_t mx4_workspace(int splits, int64_t rows, int64_t outs) {
+  return splits > 1 ? (size_t)(splits * mx4_partial(rows, outs) * 4) : 0;
 }
 
 size_t ma_mx4_matmul_workspace_size(int64_t rows, int64_t outs, int64_t ins, int32_t x_bits) {
   if (mx4_matmul_sizes("ma_mx4_matmul_workspace_size", rows, outs, ins, x_bits)) return 0;
-  return 0;
+  return mx4_workspace(mx4_plan(rows, outs, ins, x_bits).splits, rows, outs);
 }
 
 int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int64_t rows, const uint8_t* wq, const uint8_t* wscale,
@@ -388,7 +392,8 @@ int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int6
   EntryMark mark(fn);
   int rc;
   if ((rc = mx4_matmul_sizes(fn, rows, outs, ins, x_bits)) || (rc = check_dtype(fn, "y", y_dtype)) || (rc = check_flag(fn, accumulate))) return rc;
-  const size_t need = 0;
+  const Mx4Plan plan = mx4_plan(rows, outs, ins, x_bits);
+  const size_t need = mx4_workspace(plan.splits, rows, outs);
   const int64_t tiles = mx4_tiles(ins);
   const Buf bufs[] = {{xq, rows * tiles * (x_bits == 8 ? 128 : 64), 16, false, false, "xq"},
                       {xscale, rows * tiles * (x_bits == 8 ? 1 : 4), x_bits == 8 ? 1 : 4, false, false, "xscale"},
@@ -400,7 +405,8 @@ int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int6
   if (rows == 0) return MA_OK;
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const Mx4MatmulArgs a{xq, xscale, wq, wscale, y, rows, (int32_t)outs, (int32_t)ins, accumulate};
+  const Mx4MatmulArgs a{xq, xscale, wq, wscale, y, reinterpret_cast<float*>(workspace), rows, (int32_t)outs, (int32_t)ins, accumulate,
+                        plan.edge, plan.splits};
   ProfScope ps(MA_K_MX4_MATMUL, s);
   return done(launch_mx4_matmul(a, x_bits, y_dtype, s), fn);
 }

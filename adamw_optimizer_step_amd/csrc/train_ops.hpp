@@ -136,9 +136,14 @@ struct Mx4MatmulArgs {
   const uint8_t *xq, *xscale;   // rows x ins, in 4 bits or 8
   const uint8_t *wq, *wscale;   // outs x ins, in 4 bits
   void* y;                      // rows x outs
+  float* partial;               // [splits][mx4_partial], splits > 1
   int64_t rows;
-  int32_t outs, ins, accumulate;
+  int32_t outs, ins, accumulate, edge, splits;   // edge, splits: mx4_plan's
 };
+struct Mx4Plan { int edge, splits; };   // edge of the output tile; 0: 16 outputs of few rows
+// elements of one split's partial products (whole cache lines)
+__host__ __device__ constexpr int64_t mx4_partial(int64_t rows, int64_t outs) { return round_up(rows * outs, 64); }
+Mx4Plan mx4_plan(int64_t rows, int64_t outs, int64_t ins, int x_bits);
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int x_bits, int y_dt, hipStream_t s);
 
 // ---- weight gradient out of a checkpoint ----

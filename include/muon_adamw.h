@@ -495,8 +495,8 @@ int ma_mx4_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
  * (x_bits 4) or as an 8-bit checkpoint (x_bits 8). The held values are multiplied as
  * they are; sums are fp32, y (rows x outs) is rounded once. A NaN that is held
  * reaches every output of its row (of w: of its column).
- * Limits: rows <= 2^24, outs, ins <= 2^23, rows * outs <= 2^33, rows * P and outs * P
- * <= 2^36 (P = ins rounded up to a multiple of MA_MX4_TILE). workspace: at least ma_mx4_matmul_workspace_size
+ * Limits: rows <= 2^24, outs, ins <= 2^23, rows * outs, rows * P and outs * P <= 2^36
+ * (P = ins rounded up to a multiple of MA_MX4_TILE). workspace: at least ma_mx4_matmul_workspace_size
  * bytes, which may be 0; that is the need of exactly these sizes. */
 size_t ma_mx4_matmul_workspace_size(int64_t rows, int64_t outs, int64_t ins, int32_t x_bits);
 int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int64_t rows, const uint8_t* wq,
