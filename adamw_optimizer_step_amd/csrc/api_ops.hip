@@ -406,7 +406,7 @@ int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int6
   if ((rc = check_stream_device(stream, "the stream"))) return rc;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const Mx4MatmulArgs a{xq, xscale, wq, wscale, y, reinterpret_cast<float*>(workspace), rows, (int32_t)outs, (int32_t)ins, accumulate,
-                        plan.edge, plan.splits};
+                        plan.edge, plan.splits, rows * outs * dt_size(y_dtype) > kStreamBytes};
   ProfScope ps(MA_K_MX4_MATMUL, s);
   return done(launch_mx4_matmul(a, x_bits, y_dtype, s), fn);
 }

@@ -5,6 +5,7 @@
 // operands are e2m1 or e4m3 values with a power of two for every 32 k, and whose
 // sums are fp32. Nothing is unpacked; products of held values are exact.
 #include <type_traits>
+#include <utility>
 
 #include "mx4.hpp"
 #include "train_ops.hpp"
@@ -98,34 +99,42 @@ static hipError_t mx4_rows(const Mx4MatmulArgs& a, int waves, hipStream_t s) {
 
 // ---------------------------------------------------------------------------
 // Many rows: output tiles of BM rows m and BN outputs n, by WGM x WGN waves of FM x FN
-// blocks of 32 x 32.
+// blocks of 16 x 16.
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) unsigned char lds_u8_t;
 
-// BYTES per lane from memory into LDS, the lanes' side by side from `to` (the same for
-// every lane); a single byte as a word.
+// 16 bytes per lane from memory, at base + off, into LDS, the lanes' side by side from `to` (base
+// and `to` the same for every lane). In assembler, as the compiler waits for all LDS reads at
+// each one's use where it knows of such a copy under way. Nothing is loaded into a register.
+__device__ __forceinline__ void copy_chunks(const uint8_t* base, uint32_t off, lds_u8_t* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(at), "v"(off), "s"(base) : "memory");
+}
+// A word, or a byte as a word, of the first 32 lanes.
 template <int BYTES>
-__device__ __forceinline__ void copy_lds(const uint8_t* from, lds_u8_t* to) {
-  static_assert(BYTES == 16 || BYTES == 4 || BYTES == 1, "a chunk, a word or a byte");
-  if constexpr (BYTES == 16) __builtin_amdgcn_global_load_lds(from, (lds_void_t*)to, 16, 0, 0);
-  else if constexpr (BYTES == 4) __builtin_amdgcn_global_load_lds(from, (lds_void_t*)to, 4, 0, 0);
-  else __builtin_amdgcn_global_load_lds(from, (lds_void_t*)to, 1, 0, 0);
+__device__ __forceinline__ void copy_words(const uint8_t* base, uint32_t off, lds_u8_t* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
+  uint64_t all;
+#define MA_COPY(op) \
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, exec\n\ts_mov_b32 exec_hi, 0\n\t" op " %2, %3\n\ts_mov_b64 exec, %0" : "=&s"(all) : "s"(at), "v"(off), "s"(base) : "memory")
+  if constexpr (BYTES == 4) MA_COPY("global_load_lds_dword");
+  else MA_COPY("global_load_lds_ubyte");
+#undef MA_COPY
 }
 
 template <int XB_, int WGM_, int WGN_, int FM_, int FN_, int STAGES_>
 struct Mx4Tile {
   static constexpr int XB = XB_, WGM = WGM_, WGN = WGN_, FM = FM_, FN = FN_, STAGES = STAGES_;
-  static constexpr int WTM = FM * 32, WTN = FN * 32, BM = WGM * WTM, BN = WGN * WTN, NW = WGM * WGN, NT = NW * 64;
+  static constexpr int WTM = FM * 16, WTN = FN * 16, BM = WGM * WTM, BN = WGN * WTN, NW = WGM * WGN, NT = NW * 64;
   static constexpr int XR = XB == 8 ? 128 : 64, WR = 64;   // bytes of a row's k-tile
   // a stage: x's rows, w's rows, and a word of scales for each of them
   static constexpr int W_AT = BM * XR, S_AT = W_AT + BN * WR, STAGE = S_AT + (BM + BN) * 4;
-  // copies of 1024 bytes (64 words of scales) per wave and k-tile
-  static constexpr int NX = BM * XR / 1024 / NW, NWT = BN * WR / 1024 / NW, NS = (BM + BN) / 64 / NW, COPIES = NX + NWT + NS;
-  static constexpr int LDE = WTN + 4;   // epilogue staging pitch (floats)
-  static_assert(NX * NW * 1024 == BM * XR && NWT * NW * 1024 == BN * WR && NS * NW * 64 == BM + BN, "whole copies");
-  static_assert((STAGES - 1) * COPIES <= 63, "vmcnt's range");
-  static_assert(NW * 32 * LDE * 4 <= STAGES * STAGE && STAGES * STAGE <= 160 * 1024, "LDS");
+  // copies of 1024 bytes, and of 32 rows' scales of each operand, per wave and k-tile
+  static constexpr int NX = BM * XR / 1024 / NW, NWT = BN * WR / 1024 / NW, COPIES = NX + NWT + 2;
+  static constexpr int BLOCKS = STAGES * STAGE > 80 * 1024 ? 1 : 2;   // per CU
+  static_assert(NX * NW * 1024 == BM * XR && NWT * NW * 1024 == BN * WR && BM == 32 * NW && BN == 32 * NW, "whole copies");
+  static_assert((STAGES - 1) * COPIES <= 63 && STAGES >= 3 && STAGES <= 4, "vmcnt's range, the waits");
+  static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
 };
 
 // Until at most N of this wave's memory accesses are outstanding (they end in order).
@@ -134,238 +143,391 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// One block per output tile and split of the k-tiles.
+// This wave's LDS reads are done, then the block's barrier.
+__device__ __forceinline__ void block_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc += w x, 16 x 16 outputs and 128 k, in place: from the builtin the compiler makes a new
+// accumulator each time, and moves them all. ACC_A: they are in the accumulation registers.
+// FRESH: a scale may have been computed by the instruction before, which needs two wait states.
+// Whoever reads acc otherwise calls settled() first.
+template <int XB> struct MxRow { typedef u32x4_t T; };   // a lane's 32 values of x
+template <> struct MxRow<8> { typedef i32x8_t T; };
+template <int XB, bool ACC_A, bool FRESH>
+__device__ __forceinline__ void mx_mfma16_into(f32x4_t& acc, u32x4_t w, typename MxRow<XB>::T x, int ws, int xs) {
+#if defined(__HIP_DEVICE_COMPILE__)   // (the host's pass knows other registers)
+#define MA_MFMA(wait, c, fmt)                                                                                                \
+  asm volatile(wait "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:" fmt : c(acc) : "v"(w), "v"(x), "v"(ws), "v"(xs))
+  if constexpr (XB == 8) {
+    if constexpr (ACC_A) { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+a", "0"); else MA_MFMA("", "+a", "0"); }
+    else { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+v", "0"); else MA_MFMA("", "+v", "0"); }
+  } else {
+    if constexpr (ACC_A) { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+a", "4"); else MA_MFMA("", "+a", "4"); }
+    else { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+v", "4"); else MA_MFMA("", "+v", "4"); }
+  }
+#undef MA_MFMA
+#endif
+}
+
+// The MFMAs into these 4 accumulators are done: 16 passes and more have gone by.
+template <bool ACC_A>
+__device__ __forceinline__ void settled(f32x4_t& a, f32x4_t& b, f32x4_t& c, f32x4_t& d) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (ACC_A) asm volatile("s_nop 15\n\ts_nop 7" : "+a"(a), "+a"(b), "+a"(c), "+a"(d));
+  else asm volatile("s_nop 15\n\ts_nop 7" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+#endif
+}
+
+// What a row's chunks of 16 bytes are exchanged by. A read of a fragment takes 16 rows at 4
+// chunks g, lane 16 g + r; LDS serves lanes 0-3, 12-15 and 20-27 together, then 4-11, 16-19
+// and 28-31, the others alike: rows 0-3 and 12-15 at one chunk beside rows 4-11 at the next.
+// With these values each time all 64 banks are met once.
+template <int CHUNKS>
+__device__ __forceinline__ int spread(int r) {
+  return CHUNKS == 8 ? ((r >> 1) + 2) & 7 : -(r >> 2) & 3;
+}
+
+// f(0), f(1), .. f(N - 1), each with its number as a constant.
+template <typename F, int... I>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each(f, std::make_integer_sequence<int, N>());
+}
+
+// 8 consecutive outputs per lane of 16 x 32: from two blocks' accumulators, where lane (l16, g)
+// has outputs 4 g .. 4 g + 3 of its row, those of 8 g .. 8 g + 7 as packed bf16.
+__device__ __forceinline__ u32x4_t pack_pair(const f32x4_t& a, const f32x4_t& b) {
+  typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+  uint32_t lo[2], hi[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = pack_bf16x2(a[2 * i], a[2 * i + 1]), y = pack_bf16x2(b[2 * i], b[2 * i + 1]);
+    const u32x2_t u = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(x, y, false, false));
+    const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(u.x, u.y, false, false));
+    lo[i] = v.x;
+    hi[i] = v.y;
+  }
+  return u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// Of two parts of 16 rows, in which lane (l16, g) has chunk g of row l16: the first 8 rows of both
+// side by side, lanes 8 .. 15 of each 16 having p's last rows' place taken by q's first, and the last 8.
+__device__ __forceinline__ void rows_side_by_side(u32x4_t& p, u32x4_t& q) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = (int)p[i], b = (int)q[i];
+    p[i] = (uint32_t)__builtin_amdgcn_update_dpp(a, b, 0x128, 0xF, 0xC, false);   // lanes 8..15 from 8 lanes below, of q
+    q[i] = (uint32_t)__builtin_amdgcn_update_dpp(b, a, 0x128, 0xF, 0x3, false);   // lanes 0..7 from 8 above, of p
+  }
+}
+
+// An output tile and split of the k-tiles.
+struct Mx4Job {
+  int m0, n0, split, v0, v1;
+};
+
+// Persistent blocks, each of which works on a list of output tiles.
 //
 // LDS holds a ring of STAGES k-tiles of both operands as they are in memory, with
-// their scales, copied there directly. Rows are 4 (8 bits: 8) chunks of 16 bytes, and
-// 16 lanes of a read take 16 rows at one chunk: chunk c of row r lies at c ^ (r / 4)
-// (c ^ (r / 2)), which spreads them over all banks. While the first half of k-tile t
-// is multiplied, the second half's fragments are read; before the second half, k-tile
-// t + 1 has landed and one barrier says so to every wave, after which its first
-// fragments are read and k-tile t + STAGES is sent for into the stage just read.
+// their scales, copied there directly. Rows are 4 (8 bits: 8) chunks of 16 bytes; chunk c
+// of row r lies at c ^ spread(r), see there.
+//
+// A k-tile's MFMAs go by pairs of x's blocks and, within a pair, w's blocks. In the first
+// half of them x of the later pairs is read; then the next k-tile has landed and one barrier
+// says so to every wave, and that every wave has read all of this one. In the second half the
+// first pair of x of the next k-tile is read, and w's blocks take the place of the present ones
+// as the last pair is done with them. Copies of the k-tile STAGES further into the stage just
+// read are spread over the k-tile's length from there. The loop turns at the barrier, where
+// nothing is under way from LDS: at a turn the compiler waits for all that is.
+//
+// The k-tiles of one output tile follow on those of the one before: its first ones are copied,
+// and its first fragments read, before the results are stored, and the stores end while it is
+// worked on. Results go from the registers to memory, without LDS or a barrier.
 template <typename TL, int YD>
-__global__ void __launch_bounds__(TL::NT, TL::STAGES * TL::STAGE > 80 * 1024 ? TL::NW / 4 : TL::NW / 2) k_mx4_tile(const Mx4MatmulArgs a) {
+__global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(const Mx4MatmulArgs a) {
   constexpr int XB = TL::XB, FM = TL::FM, FN = TL::FN, S = TL::STAGES;
-  constexpr int XC = TL::XR / 16, XV = XB == 8 ? 2 : 1;   // chunks of a row, chunks per fragment
+  constexpr int XC = TL::XR / 16;   // chunks of a row
+  constexpr bool ACC_A = FM * FN > 32;   // 256 accumulators per lane are all the accumulation registers
   __shared__ __attribute__((aligned(1024))) unsigned char smem[S * TL::STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / TL::WGN, wn = wave % TL::WGN, l32 = lane & 31, g = lane >> 5;
+  const int wm = wave / TL::WGN, wn = wave % TL::WGN, l16 = lane & 15, g = lane >> 4;
+  const int kt = (int)mx4_tiles(a.ins);
 
-  // job: split-major, then bands of 4 tile rows walked column by column; XCD b % 8
-  // takes a contiguous eighth, so that its 32 CUs work on 4 x 8 tiles that share 4
-  // panels of x and 8 of w in its L2
-  const int64_t tm = (a.rows + TL::BM - 1) / TL::BM, tn = (a.outs + TL::BN - 1) / TL::BN, tiles = tm * tn;
-  const int64_t jobs = tiles * a.splits, per = (jobs + 7) / 8;
-  const int64_t job = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (job >= jobs) return;
-  const int split = (int)(job / tiles);
-  const int64_t t = job - split * tiles, band = t / (4 * tn), rem = tm - band * 4, bh = rem < 4 ? rem : 4, idx = t - band * 4 * tn;
-  const int64_t m0 = (band * 4 + idx % bh) * TL::BM, n0 = idx / bh * TL::BN;
-  const int kt = (int)mx4_tiles(a.ins), v0 = (int)((int64_t)kt * split / a.splits), v1 = (int)((int64_t)kt * (split + 1) / a.splits);
+  // jobs: split-major, then bands of 4 tile rows walked column by column; XCD b % 8
+  // takes a contiguous eighth, and its blocks every 32nd (64th) of it: at a time they work
+  // on 4 x 8 tiles that share 4 panels of x and 8 of w in its L2
+  // (fewer than 2^29 jobs)
+  const int tm = (int)((a.rows + TL::BM - 1) / TL::BM), tn = (a.outs + TL::BN - 1) / TL::BN, tiles = tm * tn;
+  const int jobs = tiles * a.splits, per = (jobs + 7) / 8, first_job = (int)(blockIdx.x % 8) * per;
+  const int end_job = first_job + per < jobs ? first_job + per : jobs, stride = (int)(gridDim.x / 8);
+  // (divisions leave the scalar registers)
+  auto scalar = [](int x) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(x); };
+  auto job_at = [&](int job) __attribute__((always_inline)) {
+    Mx4Job j;
+    j.split = scalar(job / tiles);
+    const int t = job - j.split * tiles, band = scalar(t / (4 * tn)), rem = tm - band * 4, bh = rem < 4 ? rem : 4, idx = t - band * 4 * tn;
+    const int column = scalar(idx / bh);
+    j.m0 = (band * 4 + idx - column * bh) * TL::BM;
+    j.n0 = column * TL::BN;
+    j.v0 = scalar((int)((int64_t)kt * j.split / a.splits));
+    j.v1 = scalar((int)((int64_t)kt * (j.split + 1) / a.splits));
+    return j;
+  };
+  int job = first_job + (int)(blockIdx.x / 8);
+  if (job >= end_job) return;
 
-  // this lane's place in each of its wave's copies: a 32-bit offset from the tile's first
-  // row (rows past the end are read from the last one; their results are not stored)
-  const int mlast = (int)(a.rows - m0 < TL::BM ? a.rows - m0 : TL::BM) - 1, nlast = (int)(a.outs - n0 < TL::BN ? a.outs - n0 : TL::BN) - 1;
-  uint32_t xoff[TL::NX], woff[TL::NWT], soff[TL::NS];
-#pragma unroll
-  for (int q = 0; q < TL::NX; ++q) {
-    const int r = (wave * TL::NX + q) * (64 / XC) + lane / XC, c = (lane % XC) ^ (XB == 8 ? (r >> 1) & 7 : (r >> 2) & 3);
-    xoff[q] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)(kt * TL::XR) + (uint32_t)c * 16;
-  }
-#pragma unroll
-  for (int q = 0; q < TL::NWT; ++q) {
-    const int r = (wave * TL::NWT + q) * 16 + lane / 4, c = (lane % 4) ^ ((r >> 2) & 3);
-    woff[q] = (uint32_t)(r < nlast ? r : nlast) * (uint32_t)(kt * TL::WR) + (uint32_t)c * 16;
-  }
-#pragma unroll
-  for (int q = 0; q < TL::NS; ++q) {
-    const int r = (wave * TL::NS + q) * 64 + lane, rx = r < mlast ? r : mlast, rw = r - TL::BM < nlast ? r - TL::BM : nlast;
-    soff[q] = r < TL::BM ? (uint32_t)rx * (XB == 8 ? (uint32_t)kt : 4u) : (uint32_t)rw * 4;
-  }
-  const uint8_t* const xq = a.xq + m0 * kt * TL::XR;
-  const uint8_t* const wq = a.wq + n0 * kt * TL::WR;
-  const uint8_t* const xs = a.xscale + m0 * (XB == 8 ? kt : 4);
-  const uint8_t* const ws = a.wscale + n0 * 4;
+  // where the copies are: the next k-tile's rows and scales, how many k-tiles of the job are left,
+  // and this lane's place in each of its wave's copies, a 32-bit offset from the tile's first row
+  // (rows past the end are read from the last one; their results are not stored)
+  const uint8_t *xq, *wq, *xs, *ws;
+  int left;
+  uint32_t xoff[TL::NX], woff[TL::NWT], sxoff, swoff;
   const int64_t xs_step = XB == 8 ? 1 : a.rows * 4, ws_step = (int64_t)a.outs * 4;
+  auto copies_of = [&](const Mx4Job& j) __attribute__((always_inline)) {
+    const int mlast = (int)(a.rows - j.m0 < TL::BM ? a.rows - j.m0 : TL::BM) - 1, nlast = (int)(a.outs - j.n0 < TL::BN ? a.outs - j.n0 : TL::BN) - 1;
+#pragma unroll
+    for (int q = 0; q < TL::NX; ++q) {
+      const int r = (wave * TL::NX + q) * (64 / XC) + lane / XC, c = (lane % XC) ^ spread<XC>(r);
+      xoff[q] = (uint32_t)(r < mlast ? r : mlast) * (uint32_t)(kt * TL::XR) + (uint32_t)c * 16;
+    }
+#pragma unroll
+    for (int q = 0; q < TL::NWT; ++q) {
+      const int r = (wave * TL::NWT + q) * 16 + lane / 4, c = (lane % 4) ^ spread<4>(r);
+      woff[q] = (uint32_t)(r < nlast ? r : nlast) * (uint32_t)(kt * TL::WR) + (uint32_t)c * 16;
+    }
+    const int r = wave * 32 + (lane & 31);
+    sxoff = (uint32_t)(r < mlast ? r : mlast) * (XB == 8 ? (uint32_t)kt : 4u);
+    swoff = (uint32_t)(r < nlast ? r : nlast) * 4u;
+    xq = a.xq + ((int64_t)j.m0 * kt + j.v0) * TL::XR;
+    wq = a.wq + ((int64_t)j.n0 * kt + j.v0) * TL::WR;
+    xs = a.xscale + (XB == 8 ? (int64_t)j.m0 * kt + j.v0 : (j.v0 * a.rows + j.m0) * 4);
+    ws = a.wscale + ((int64_t)j.v0 * a.outs + j.n0) * 4;
+    left = j.v1 - j.v0;
+  };
   lds_u8_t* const lds = (lds_u8_t*)smem;
-  // copy i of this wave's share of k-tile v
-  auto copy = [&](int v, lds_u8_t* st, int i) __attribute__((always_inline)) {
-    if (i < TL::NX) {
-      copy_lds<16>(xq + (int64_t)v * TL::XR + xoff[i], st + (wave * TL::NX + i) * 1024);
-    } else if (i < TL::NX + TL::NWT) {
-      const int q = i - TL::NX;
-      copy_lds<16>(wq + (int64_t)v * TL::WR + woff[q], st + TL::W_AT + (wave * TL::NWT + q) * 1024);
-    } else {
-      const int q = i - TL::NX - TL::NWT, r = (wave * TL::NS + q) * 64;
-      lds_u8_t* const to = st + TL::S_AT + r * 4;
-      if (r >= TL::BM) copy_lds<4>(ws + v * ws_step + soff[q], to);
-      else copy_lds<XB == 8 ? 1 : 4>(xs + v * xs_step + soff[q], to);
+  // copy i of this wave's share of the next k-tile
+  auto copy = [&](lds_u8_t* st, int i) __attribute__((always_inline)) {
+    if (i < TL::NX) copy_chunks(xq, xoff[i], st + (wave * TL::NX + i) * 1024);
+    else if (i < TL::NX + TL::NWT) copy_chunks(wq, woff[i - TL::NX], st + TL::W_AT + (wave * TL::NWT + i - TL::NX) * 1024);
+    else if (i == TL::NX + TL::NWT) copy_words<XB == 8 ? 1 : 4>(xs, sxoff, st + TL::S_AT + wave * 128);
+    else copy_words<4>(ws, swoff, st + TL::S_AT + TL::BM * 4 + wave * 128);
+  };
+  int copy_job = job;
+  // on to the next k-tile, of the next job after the last; behind the last job the last k-tile
+  // is copied again, to no use
+  auto copied = [&]() __attribute__((always_inline)) {
+    if (--left > 0) {
+      xq += TL::XR;
+      wq += TL::WR;
+      xs += xs_step;
+      ws += ws_step;
+    } else if (copy_job + stride < end_job) {
+      copy_job += stride;
+      copies_of(job_at(copy_job));
     }
   };
 
-  f32x16_t acc[FM][FN];
+  f32x4_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // fragments of half h of a k-tile: lane (l32, g) holds row l32 of each block and 32 values
-  // from 64 h + 32 g (8 bits: two times 16, from 64 h + 16 g and 32 further)
-  u32x4_t fx[2][FM][XV], fw[2][FN];
-  int sx[FM], sw[FN], nx[FM], nw[FN];   // this k-tile's scales, and the next one's as they are in LDS
-  int xat[FM], wat[FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i) xat[i] = (wm * TL::WTM + i * 32 + l32) * TL::XR;
-#pragma unroll
-  for (int j = 0; j < FN; ++j) wat[j] = TL::W_AT + (wn * TL::WTN + j * 32 + l32) * TL::WR;
-  const int swx = XB == 8 ? (l32 >> 1) & 7 : (l32 >> 2) & 3, sww = (l32 >> 2) & 3;
-  constexpr int READS = FM * XV + FN;
-  auto read = [&](lds_u8_t* st, int h, int i) __attribute__((always_inline)) {
-    typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
-    if (i < FM * XV) {
-      const int c = XB == 8 ? 4 * h + 2 * (i % XV) + g : 2 * h + g;
-      fx[h][i / XV][i % XV] = *(lds_u32x4_t*)(st + xat[i / XV] + ((c ^ swx) << 4));
+  // fragments: lane (l16, g) holds row l16 of each block and 32 values from 32 g (8 bits: two
+  // times 16, from 16 g and 64 further), and their scale
+  typename MxRow<XB>::T fx[FM];
+  u32x4_t fw[FN];
+  int rx[FM], rw[FN], sx[2], sw[FN];   // words of scales as they are in LDS; a pair's and w's, moved down to the lane's byte
+  const int swx = spread<XC>(l16), sww = spread<4>(l16);
+  const int xat = (wm * TL::WTM + l16) * TL::XR, wat = TL::W_AT + (wn * TL::WTN + l16) * TL::WR + ((g ^ sww) << 4);
+  const int xat0 = xat + ((g ^ swx) << 4), xat1 = xat + (((4 + g) ^ swx) << 4);
+  const int sxat = TL::S_AT + (wm * TL::WTM + l16) * 4, swat = TL::S_AT + (TL::BM + wn * TL::WTN + l16) * 4;
+  typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
+  typedef __attribute__((address_space(3))) int lds_int_t;
+  auto read_x = [&](lds_u8_t* st, int i) __attribute__((always_inline)) {
+    const u32x4_t lo = *(lds_u32x4_t*)(st + xat0 + i * 16 * TL::XR);
+    if constexpr (XB == 8) {
+      const u32x4_t hi = *(lds_u32x4_t*)(st + xat1 + i * 16 * TL::XR);
+      fx[i] = i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
     } else {
-      fw[h][i - FM * XV] = *(lds_u32x4_t*)(st + wat[i - FM * XV] + (((2 * h + g) ^ sww) << 4));
+      fx[i] = lo;
     }
   };
-  auto scales = [&](lds_u8_t* st, int i) __attribute__((always_inline)) {
-    typedef __attribute__((address_space(3))) int lds_int_t;
-    if (i < FM) nx[i] = *(lds_int_t*)(st + TL::S_AT + (wm * TL::WTM + i * 32 + l32) * 4);
-    else nw[i - FM] = *(lds_int_t*)(st + TL::S_AT + (TL::BM + wn * TL::WTN + (i - FM) * 32 + l32) * 4);
+  auto read_sx = [&](lds_u8_t* st, int i) __attribute__((always_inline)) { rx[i] = *(lds_int_t*)(st + sxat + i * 64); };
+  auto read_w = [&](lds_u8_t* st, int j) __attribute__((always_inline)) {
+    fw[j] = *(lds_u32x4_t*)(st + wat + j * 16 * TL::WR);
+    rw[j] = *(lds_int_t*)(st + swat + j * 64);
   };
-  // byte 2 h of a word moved down by g bytes is the lane's
-  auto take = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i) sx[i] = XB == 4 ? (int)((unsigned)nx[i] >> (8 * g)) : nx[i];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) sw[j] = (int)((unsigned)nw[j] >> (8 * g));
-  };
-  auto multiply = [&](auto half, int i, int j) __attribute__((always_inline)) {
-    constexpr int h = decltype(half)::value;
-    const u32x4_t &u = fw[h][j], &x0 = fx[h][i][0], &x1 = fx[h][i][XV - 1];
-    const i32x8_t w = {(int)u[0], (int)u[1], (int)u[2], (int)u[3], 0, 0, 0, 0};
-    const i32x8_t x = XB == 8 ? i32x8_t{(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]}
-                              : i32x8_t{(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], 0, 0, 0, 0};
-    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc[i][j], kFmt4, XB == 8 ? kFmt8 : kFmt4, 2 * h, sw[j], XB == 8 ? 0 : 2 * h, sx[i]);
-  };
-  typedef std::integral_constant<int, 0> First;
-  typedef std::integral_constant<int, 1> Second;
-  // reads per MFMA: the last one is sent for well before its half ends
-  constexpr int MM = FM * FN, PACE = (READS + MM / 2 - 1) / (MM / 2);
+  constexpr int MM = FM * FN, HALF = MM / 2, LATER = 2 * (FM - 2);   // LATER: reads of x and scales in the first half
+  // copies after every SPACE-th MFMA from the barrier on
+  constexpr int SPACE = MM / TL::COPIES;
+  static_assert(SPACE >= 1 && FM >= 4 && FM % 4 == 0 && LATER <= HALF * 3 / 4, "copies and reads fit between the MFMAs");
 
-  // k-tile v, its first fragments and scales in registers. FILL: k-tile v + S exists.
-  lds_u8_t* cur = lds;
-  auto tile = [&](int v, auto fill) __attribute__((always_inline)) {
-    constexpr bool FILL = decltype(fill)::value;
-    lds_u8_t* const nxt = cur == lds + (S - 1) * TL::STAGE ? lds : cur + TL::STAGE;
-#pragma unroll
-    for (int k = 0; k < MM; ++k) {
-      multiply(First(), k / FN, k % FN);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = k * PACE; i < (k + 1) * PACE && i < READS; ++i) read(cur, 1, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): this wave has read all of k-tile v
-    const bool more = FILL || v + 1 < v1;
-    if (more) {
-      if (FILL) {
-        wait_vm<(S - 2) * TL::COPIES>();
-      } else {
-        const int later = v1 - 2 - v;   // k-tiles sent for after v + 1
-        if (later >= 2 && S > 3) wait_vm<(S > 3 ? 2 : 0) * TL::COPIES>();
-        else if (later >= 1 && S > 2) wait_vm<(S > 2 ? 1 : 0) * TL::COPIES>();
-        else wait_vm<0>();
-      }
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-    }
+  // MFMA k of a k-tile, from the scales' words on
+  auto step = [&](auto number) __attribute__((always_inline)) {
+    constexpr int k = decltype(number)::value, i = k / (2 * FN) * 2 + k % 2, j = k % (2 * FN) / 2;
+    if constexpr (i == 0) sw[j] = (int)((unsigned)rw[j] >> (8 * g));
+    if constexpr (j == 0) sx[i % 2] = XB == 8 ? rx[i] : (int)((unsigned)rx[i] >> (8 * g));
+    mx_mfma16_into<XB, ACC_A, i == 0 || j == 0>(acc[i][j], fw[j], fx[i], sw[j], sx[i % 2]);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int k = 0; k < MM; ++k) {
-      multiply(Second(), k / FN, k % FN);
-      __builtin_amdgcn_sched_barrier(0);
-      if (more) {
-        constexpr int ALL = FM + FN + READS;
-#pragma unroll
-        for (int i = k * 2 * PACE; i < (k + 1) * 2 * PACE && i < ALL; ++i) {
-          if (i < FM + FN) scales(nxt, i);
-          else read(nxt, 0, i - FM - FN);
-        }
-      }
-      if (FILL) {
-#pragma unroll
-        for (int i = k * TL::COPIES / MM; i < (k + 1) * TL::COPIES / MM; ++i) copy(v + S, cur, i);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    take();
-    cur = nxt;
   };
-  typedef std::integral_constant<bool, true> Fill;
-  typedef std::integral_constant<bool, false> Last;
+  // the first half of the k-tile in stage `cur`, its w and first x in registers; copies to `to` go on
+  auto first = [&](lds_u8_t* cur, lds_u8_t* to, auto copies) __attribute__((always_inline)) {
+    each<HALF>([&](auto number) __attribute__((always_inline)) {
+      constexpr int k = decltype(number)::value, q = k + HALF;
+      step(number);
+      each<LATER>([&](auto n) __attribute__((always_inline)) {
+        constexpr int b = decltype(n)::value;
+        if constexpr (b * (HALF * 3 / 4) / LATER == k) {
+          if constexpr (b % 2 == 0) read_x(cur, 2 + b / 2);
+          else read_sx(cur, 2 + b / 2);
+        }
+      });
+      if constexpr (decltype(copies)::value && q % SPACE == 0 && q / SPACE < TL::COPIES) copy(to, q / SPACE);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // the second half, and the first reads of the next k-tile, in `nxt`
+  auto second = [&](lds_u8_t* cur, lds_u8_t* nxt) __attribute__((always_inline)) {
+    each<HALF>([&](auto number) __attribute__((always_inline)) {
+      constexpr int q = decltype(number)::value, k = q + HALF;
+      step(std::integral_constant<int, k>());
+      if constexpr (q < 2) read_x(nxt, q);
+      else if constexpr (q < 4) read_sx(nxt, q - 2);
+      if constexpr (k >= MM - 2 * FN && k % 2 == 1) read_w(nxt, k % (2 * FN) / 2);
+      if constexpr (q % SPACE == 0 && q / SPACE < TL::COPIES) copy(cur, q / SPACE);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  // Results of a job, and zeros in their place: 16 bytes per lane (8 where bf16 is added to) and
+  // whole lines, of 8 rows at a time.
+  auto store = [&](const Mx4Job& j) __attribute__((always_inline)) {
+    const int at_m = j.m0 + wm * TL::WTM + (l16 & 7), at_n = j.n0 + wn * TL::WTN;
+    auto put = [&](auto type, auto adds, auto past) __attribute__((always_inline)) {
+      constexpr int OD = decltype(type)::value;
+      constexpr bool ADD = decltype(adds)::value, PAIRS = OD == DT_BF16 && !ADD, NT = decltype(past)::value;
+      constexpr int E = PAIRS ? 8 : 4, W = PAIRS ? 4 : 2;   // outputs per lane; blocks that are side by side
+      unsigned char* const base = a.splits > 1 ? elem_ptr<OD>(a.partial, j.split * mx4_partial(a.rows, a.outs)) : reinterpret_cast<unsigned char*>(a.y);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int b = 0; b < FN; b += 4) settled<ACC_A>(acc[i][b], acc[i][b + 1], acc[i][b + 2], acc[i][b + 3]);
+#pragma unroll
+        for (int b = 0; b < FN; b += W) {
+          u32x4_t part[2];
+          if constexpr (PAIRS) {
+            part[0] = pack_pair(acc[i][b], acc[i][b + 1]);
+            part[1] = pack_pair(acc[i][b + 2], acc[i][b + 3]);
+          } else {
+            part[0] = __builtin_bit_cast(u32x4_t, acc[i][b]);
+            part[1] = __builtin_bit_cast(u32x4_t, acc[i][b + 1]);
+          }
+          rows_side_by_side(part[0], part[1]);
+          const int n = at_n + b * 16 + (l16 >> 3) * (W * 8) + g * E;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int64_t m = (int64_t)at_m + i * 16 + h * 8;
+            if (m >= a.rows || n >= a.outs) continue;
+            unsigned char* const row = base + m * a.outs * elem_bytes<OD>();
+            if constexpr (PAIRS) {
+              if (n + 8 <= a.outs) {
+                typedef U16<DT_BF16>::T V;
+                V* const to = reinterpret_cast<V*>(row + (int64_t)n * 2);
+                if constexpr (NT) __builtin_nontemporal_store((V)part[h], to);
+                else *to = part[h];
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (n + e < a.outs) reinterpret_cast<uint16_t*>(row)[n + e] = (uint16_t)(part[h][e / 2] >> (16 * (e % 2)));
+              }
+            } else {
+              float v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(part[h][e]);
+              if constexpr (ADD) {
+                float old[4];
+                if (n + 4 <= a.outs) {
+                  Raw4<OD> r;
+                  r.u = *reinterpret_cast<const typename Quad<OD>::T*>(row + (int64_t)n * elem_bytes<OD>());
+                  quad_f32<OD>(r, 0, 4, old);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) old[e] = n + e < a.outs ? load1<OD>(row, n + e) : 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(old[e], v[e]);
+              }
+              quad_store_row<OD, NT>(row, n, a.outs, v);
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < FN; ++b) acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    typedef std::integral_constant<int, DT_F32> F;
+    typedef std::integral_constant<int, YD> Y;
+    typedef std::integral_constant<bool, true> Yes;
+    typedef std::integral_constant<bool, false> No;
+    if (a.splits > 1) put(F(), No(), No());
+    else if (a.accumulate) put(Y(), Yes(), No());
+    else if (a.stream) put(Y(), No(), Yes());
+    else put(Y(), No(), No());
+  };
+
+  copies_of(job_at(job));
 #pragma unroll
   for (int v = 0; v < S; ++v) {
-    if (v0 + v < v1) {
 #pragma unroll
-      for (int i = 0; i < TL::COPIES; ++i) copy(v0 + v, lds + v * TL::STAGE, i);
-    }
+    for (int i = 0; i < TL::COPIES; ++i) copy(lds + v * TL::STAGE, i);
+    copied();
   }
-  if (v1 - v0 >= S) wait_vm<(S - 1) * TL::COPIES>();
-  else wait_vm<0>();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  wait_vm<(S - 1) * TL::COPIES>();
+  block_barrier();
 #pragma unroll
-  for (int i = 0; i < FM + FN; ++i) scales(lds, i);
-#pragma unroll
-  for (int i = 0; i < READS; ++i) read(lds, 0, i);
-  take();
-  int v = v0;
-  for (; v < v1 - S; ++v) tile(v, Fill());
-  for (; v < v1; ++v) tile(v, Last());
-
-  // 32 rows of the wave's block at a time through its own part of LDS, so that stores are
-  // 8 consecutive values per lane
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  float* const mine = reinterpret_cast<float*>(smem) + wave * 32 * TL::LDE;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *reinterpret_cast<float4*>(mine + l32 * TL::LDE + j * 32 + b * 8 + g * 4) =
-            make_float4(acc[i][j][4 * b], acc[i][j][4 * b + 1], acc[i][j][4 * b + 2], acc[i][j][4 * b + 3]);
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int u = 0; u < 32 * TL::WTN / 512; ++u) {
-      constexpr int LPR = TL::WTN / 8;
-      const int row = u * (64 / LPR) + lane / LPR, c = lane % LPR * 8;
-      const float4 x = *reinterpret_cast<const float4*>(mine + row * TL::LDE + c), y = *reinterpret_cast<const float4*>(mine + row * TL::LDE + c + 4);
-      float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      const int64_t m = m0 + wm * TL::WTM + i * 32 + row;
-      const int n = (int)n0 + wn * TL::WTN + c;
-      if (m >= a.rows || n >= a.outs) continue;
-      if (a.splits > 1) {
-        store_row<DT_F32>(elem_ptr<DT_F32>(a.partial, split * mx4_partial(a.rows, a.outs) + m * a.outs), n, a.outs, o);
-        continue;
-      }
-      unsigned char* out = elem_ptr<YD>(a.y, m * a.outs);
-      if (a.accumulate) {
-        float old[8];
-        raw_f32_row<YD>(raw_load_row<YD>(out, n, a.outs), n, a.outs, old);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __fadd_rn(old[e], o[e]);
-      }
-      store_row<YD>(out, n, a.outs, o);
-    }
-    __builtin_amdgcn_wave_barrier();
+  for (int i = 0; i < 2; ++i) {
+    read_x(lds, i);
+    read_sx(lds, i);
   }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) read_w(lds, j);
+  first(lds, lds, std::integral_constant<bool, false>());
+  Mx4Job now = job_at(job);
+  int more = now.v1 - now.v0;   // k-tiles of the job that are not done
+  lds_u8_t* cur = lds;
+  // After the stores of a whole tile (STORES of them at least, behind the copies that are waited for)
+  // the first turns do not wait for them; the counter does not go beyond 63.
+  constexpr int KEEP = (S - 2) * TL::COPIES, STORES = YD == DT_BF16 ? MM / 2 : MM, RELAXED = KEEP + STORES < 63 ? KEEP + STORES : 63;
+  int relaxed = 0;
+  for (;;) {
+    // the next k-tile has landed: what was sent for after it may still be under way
+    if (relaxed > 0) wait_vm<RELAXED>();
+    else wait_vm<KEEP>();
+    --relaxed;
+    block_barrier();
+    lds_u8_t *const to = cur, *const nxt = cur == lds + (S - 1) * TL::STAGE ? lds : cur + TL::STAGE;
+    second(cur, nxt);
+    if (--more == 0) {
+      store(now);
+      relaxed = now.m0 + TL::BM <= a.rows && now.n0 + TL::BN <= a.outs ? S - 2 : 0;
+      job += stride;
+      if (job >= end_job) break;
+      now = job_at(job);
+      more = now.v1 - now.v0;
+    }
+    first(nxt, to, std::integral_constant<bool, true>());
+    copied();
+    cur = nxt;
+  }
+  wait_vm<0>();   // no copy into LDS outlives the block
 }
 
 // The splits' partial products, added in order: 4 consecutive values per thread, 8
@@ -408,7 +570,8 @@ Mx4Plan mx4_plan(int64_t rows, int64_t outs, int64_t ins, int x_bits) {
 template <typename TL, int YD>
 static hipError_t mx4_tile(const Mx4MatmulArgs& a, hipStream_t s) {
   const int64_t jobs = ((a.rows + TL::BM - 1) / TL::BM) * ((a.outs + TL::BN - 1) / TL::BN) * a.splits;
-  hipLaunchKernelGGL((k_mx4_tile<TL, YD>), dim3((unsigned)((jobs + 7) / 8 * 8)), dim3(TL::NT), 0, s, a);
+  const int64_t want = (jobs + 7) / 8 * 8, most = 256 * TL::BLOCKS;   // resident blocks
+  hipLaunchKernelGGL((k_mx4_tile<TL, YD>), dim3((unsigned)(want < most ? want : most)), dim3(TL::NT), 0, s, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.splits == 1) return err;
   hipLaunchKernelGGL((k_mx4_join<YD>), dim3((unsigned)((a.rows * a.outs + 1023) / 1024)), dim3(256), 0, s, a);
@@ -417,8 +580,8 @@ static hipError_t mx4_tile(const Mx4MatmulArgs& a, hipStream_t s) {
 
 template <int XB, int YD>
 static hipError_t mx4_product(const Mx4MatmulArgs& a, hipStream_t s) {
-  if (a.edge == 256) return mx4_tile<Mx4Tile<XB, 2, 2, 4, 4, XB == 8 ? 3 : 4>, YD>(a, s);
-  if (a.edge == 128) return mx4_tile<Mx4Tile<XB, 2, 2, 2, 2, XB == 8 ? 3 : 4>, YD>(a, s);
+  if (a.edge == 256) return mx4_tile<Mx4Tile<XB, 2, 4, 8, 4, XB == 8 ? 3 : 4>, YD>(a, s);
+  if (a.edge == 128) return mx4_tile<Mx4Tile<XB, 2, 2, 4, 4, XB == 8 ? 3 : 4>, YD>(a, s);
   return a.rows <= 16 ? mx4_rows<XB, YD, 1>(a, 4, s) : mx4_rows<XB, YD, 4>(a, 4, s);
 }
 

@@ -139,6 +139,7 @@ struct Mx4MatmulArgs {
   float* partial;               // [splits][mx4_partial], splits > 1
   int64_t rows;
   int32_t outs, ins, accumulate, edge, splits;   // edge, splits: mx4_plan's
+  int32_t stream;               // whether y passes the caches
 };
 struct Mx4Plan { int edge, splits; };   // edge of the output tile; 0: 16 outputs of few rows
 // elements of one split's partial products (whole cache lines)
