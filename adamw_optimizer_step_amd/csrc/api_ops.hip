@@ -385,6 +385,17 @@ size_t ma_mx4_matmul_workspace_size(int64_t rows, int64_t outs, int64_t ins, int
   return mx4_workspace(mx4_plan(rows, outs, ins, x_bits).splits, rows, outs);
 }
 
+int ma_test_mx4_matmul_plan(int64_t rows, int64_t outs, int64_t ins, int32_t x_bits, int32_t* edge, int32_t* splits) {
+  const char* fn = "ma_test_mx4_matmul_plan";
+  int rc;
+  if ((rc = mx4_matmul_sizes(fn, rows, outs, ins, x_bits))) return rc;
+  if (!edge || !splits) return fail(MA_ERR_INVALID_ARG, "%s: edge or splits is null", fn);
+  const Mx4Plan plan = mx4_plan(rows, outs, ins, x_bits);
+  *edge = plan.edge;
+  *splits = plan.splits;
+  return MA_OK;
+}
+
 int ma_mx4_matmul(const uint8_t* xq, const uint8_t* xscale, int32_t x_bits, int64_t rows, const uint8_t* wq, const uint8_t* wscale,
                   int64_t outs, int64_t ins, void* y, int32_t y_dtype, int32_t accumulate, void* workspace, size_t workspace_bytes,
                   void* stream) {

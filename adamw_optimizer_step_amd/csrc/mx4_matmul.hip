@@ -4,6 +4,7 @@
 // on the scaled matrix instructions of gfx950: 16 x 16 outputs and 128 k each, whose
 // operands are e2m1 or e4m3 values with a power of two for every 32 k, and whose
 // sums are fp32. Nothing is unpacked; products of held values are exact.
+#include <algorithm>
 #include <type_traits>
 #include <utility>
 
@@ -21,15 +22,16 @@ __device__ __forceinline__ f32x4_t mx_mfma16(const i32x8_t& w, const i32x8_t& x,
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, kFmt4, XB == 8 ? kFmt8 : kFmt4, 0, ws, 0, xs);
 }
 
-// Few rows: a block of WAVES waves takes 16 outputs n of MB * 16 rows m, each wave a
-// contiguous share of the k-tiles; the waves' sums are added in order in LDS. The
-// operands go from memory to registers: lane l holds row l % 16 and, of every k-tile,
+// Few rows: a block takes 16 outputs n of MB * 16 rows m, each wave a contiguous share of the
+// k-tiles; the waves' sums are added in order in LDS. The operands go from memory to
+// registers, several k-tiles at once: lane l holds row l % 16 and, of every k-tile,
 // 32 values from 32 * (l / 16) (of 8-bit rows two times 16, from 16 * (l / 16) and 64
 // further: so the instruction pairs them with 4-bit ones). Rows past the end are read
 // from inside the matrix; their results are not stored.
 template <int XB, int YD, int MB>
 __global__ void __launch_bounds__(1024) k_mx4_rows(const Mx4MatmulArgs a) {
   extern __shared__ float join[];   // [waves][MB][64][4]
+  constexpr int U = MB == 1 ? 4 : 2, XV = XB == 8 ? 2 : 1;   // k-tiles in flight
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int r = lane & 15, g = lane >> 4;
   const int64_t nt = (a.outs + 15) / 16;
@@ -48,26 +50,37 @@ __global__ void __launch_bounds__(1024) k_mx4_rows(const Mx4MatmulArgs a) {
   f32x4_t acc[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int t = k0; t < k1; ++t) {
-    const u32x4_t u = *reinterpret_cast<const u32x4_t*>(wq + (int64_t)t * 64);
-    const i32x8_t w = {(int)u[0], (int)u[1], (int)u[2], (int)u[3], 0, 0, 0, 0};
-    const int sw = ws[(int64_t)t * a.outs * 4];
+  auto tiles = [&](int t, auto count) __attribute__((always_inline)) {
+    constexpr int N = decltype(count)::value;
+    u32x4_t w[N], x[N][MB][XV];
+    int sw[N], sx[N][MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      i32x8_t x;
-      int sx;
-      if constexpr (XB == 8) {
-        const u32x4_t p = *reinterpret_cast<const u32x4_t*>(xq[b] + (int64_t)t * 128), q = *reinterpret_cast<const u32x4_t*>(xq[b] + (int64_t)t * 128 + 64);
-        x = i32x8_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3], (int)q[0], (int)q[1], (int)q[2], (int)q[3]};
-        sx = xs[b][t];
-      } else {
-        const u32x4_t p = *reinterpret_cast<const u32x4_t*>(xq[b] + (int64_t)t * 64);
-        x = i32x8_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
-        sx = xs[b][(int64_t)t * a.rows * 4];
+    for (int u = 0; u < N; ++u) {
+      const int64_t at = t + u;
+      w[u] = *reinterpret_cast<const u32x4_t*>(wq + at * 64);
+      sw[u] = ws[at * a.outs * 4];
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+#pragma unroll
+        for (int v = 0; v < XV; ++v) x[u][b][v] = *reinterpret_cast<const u32x4_t*>(xq[b] + at * (64 * XV) + v * 64);
+        sx[u][b] = XB == 8 ? xs[b][at] : xs[b][at * a.rows * 4];
       }
-      acc[b] = mx_mfma16<XB>(w, x, acc[b], sw, sx);
     }
-  }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const i32x8_t w8 = {(int)w[u][0], (int)w[u][1], (int)w[u][2], (int)w[u][3], 0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const u32x4_t &p = x[u][b][0], &q = x[u][b][XV - 1];
+        const i32x8_t x8 = XB == 8 ? i32x8_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3], (int)q[0], (int)q[1], (int)q[2], (int)q[3]}
+                                   : i32x8_t{(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
+        acc[b] = mx_mfma16<XB>(w8, x8, acc[b], sw[u], sx[u][b]);
+      }
+    }
+  };
+  int t = k0;
+  for (; t + U <= k1; t += U) tiles(t, std::integral_constant<int, U>());
+  for (; t < k1; ++t) tiles(t, std::integral_constant<int, 1>());
 #pragma unroll
   for (int b = 0; b < MB; ++b) *reinterpret_cast<float4*>(join + ((wave * MB + b) * 64 + lane) * 4) = make_float4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
   __syncthreads();
@@ -88,13 +101,6 @@ __global__ void __launch_bounds__(1024) k_mx4_rows(const Mx4MatmulArgs a) {
     }
     quad_store_row<YD>(out, (int)at, (int)a.outs, v);
   }
-}
-
-template <int XB, int YD, int MB>
-static hipError_t mx4_rows(const Mx4MatmulArgs& a, int waves, hipStream_t s) {
-  const int64_t blocks = (a.outs + 15) / 16 * ((a.rows + 16 * MB - 1) / (16 * MB));
-  hipLaunchKernelGGL((k_mx4_rows<XB, YD, MB>), dim3((unsigned)blocks), dim3(64 * waves), (size_t)waves * MB * 1024, s, a);
-  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -560,11 +566,55 @@ __global__ void __launch_bounds__(256) k_mx4_join(const Mx4MatmulArgs a) {
   }
 }
 
+// Few rows: blocks of 16, 32 or 64 rows, and waves per block: 16 per CU where that leaves each 2 k-tiles.
+static int mx4_rows_mb(int64_t rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
+static int64_t mx4_rows_blocks(int64_t rows, int64_t outs) {
+  const int64_t m = 16 * mx4_rows_mb(rows);
+  return (outs + 15) / 16 * ((rows + m - 1) / m);
+}
+static int mx4_rows_waves(int64_t rows, int64_t outs, int64_t ins) {
+  const int64_t blocks = mx4_rows_blocks(rows, outs), kt = mx4_tiles(ins);
+  int waves = 1;
+  while (waves < 16 && blocks * waves < 4096 && kt >= 4 * waves) waves *= 2;
+  return waves;
+}
+
+// The form, and the splits of the k-tiles, by the time they should take (us), from what 200 sizes
+// took. Few rows' blocks each read their rows of both operands, at 7 TB/s from the caches, and 35 GB/s
+// a block. Tiles
+// have a fixed part, what the jobs take that share a CU (two small ones at a time, a big one) and the
+// partial results' way to memory and back.
+//   k-tile of 128 x 128, 4 bits 0.47 alone, 0.79 for a pair; 8 bits 0.53, 0.97
+//   k-tile of 256 x 256, 4 bits 0.93; 8 bits 1.35
 Mx4Plan mx4_plan(int64_t rows, int64_t outs, int64_t ins, int x_bits) {
-  (void)ins;
-  (void)x_bits;
-  if (rows <= 64) return {0, 1};
-  return {rows > 128 && outs > 128 ? 256 : 128, 1};
+  const bool x8 = x_bits == 8;
+  const int64_t kt = mx4_tiles(ins), blocks = mx4_rows_blocks(rows, outs);
+  const int waves = mx4_rows_waves(rows, outs, ins);
+  const double mb = (double)rows * (double)outs * 4e-6;   // of one fp32 result
+  Mx4Plan best{0, 1};
+  const int64_t in_block = rows < 16 * mx4_rows_mb(rows) ? rows : 16 * mx4_rows_mb(rows);
+  const double block = (double)kt * (1024 + (double)in_block * (x8 ? 128 : 64));   // bytes
+  double best_us = 2.7 + 0.12 * waves + (double)blocks / 730 + std::max((double)blocks * block / 7e6, (double)((blocks + 255) / 256) * block / 35e3);
+  if (blocks > ((int64_t)1 << 31) / (64 * waves)) best_us = 1e30;   // beyond a launch's threads
+  for (int edge = 128; edge <= 256; edge *= 2) {
+    const int64_t tiles = ((rows + edge - 1) / edge) * ((outs + edge - 1) / edge);
+    for (int64_t s = 1; s <= 64 && s <= kt; ++s) {
+      const int64_t jobs = tiles * s, rounds = (jobs + 255) / 256, share = (kt + s - 1) / s;
+      const double full = jobs < 256 ? (double)jobs / 256 : 1.0;
+      double us;
+      if (edge == 128) us = 3.5 + (double)(rounds / 2) * ((double)share * (x8 ? 0.97 : 0.79) + 2.2) + (double)(rounds % 2) * ((double)share * (x8 ? 0.53 : 0.47) + 1.5);
+      else us = 7.0 + (double)rounds * ((double)share * (x8 ? 1.35 : 0.93) + 5.0 * full);
+      if (s > 1) us += 4.0 + (double)s * mb * (1 / 6.0 + 1 / 9.0);
+      if (us < best_us * 0.999) { best_us = us; best = {edge, (int)s}; }
+    }
+  }
+  return best;
+}
+
+template <int XB, int YD, int MB>
+static hipError_t mx4_rows(const Mx4MatmulArgs& a, int waves, hipStream_t s) {
+  hipLaunchKernelGGL((k_mx4_rows<XB, YD, MB>), dim3((unsigned)mx4_rows_blocks(a.rows, a.outs)), dim3(64 * waves), (size_t)waves * MB * 1024, s, a);
+  return hipGetLastError();
 }
 
 template <typename TL, int YD>
@@ -582,7 +632,8 @@ template <int XB, int YD>
 static hipError_t mx4_product(const Mx4MatmulArgs& a, hipStream_t s) {
   if (a.edge == 256) return mx4_tile<Mx4Tile<XB, 2, 4, 8, 4, XB == 8 ? 3 : 4>, YD>(a, s);
   if (a.edge == 128) return mx4_tile<Mx4Tile<XB, 2, 2, 4, 4, XB == 8 ? 3 : 4>, YD>(a, s);
-  return a.rows <= 16 ? mx4_rows<XB, YD, 1>(a, 4, s) : mx4_rows<XB, YD, 4>(a, 4, s);
+  const int waves = mx4_rows_waves(a.rows, a.outs, a.ins), mb = mx4_rows_mb(a.rows);
+  return mb == 1 ? mx4_rows<XB, YD, 1>(a, waves, s) : (mb == 2 ? mx4_rows<XB, YD, 2>(a, waves, s) : mx4_rows<XB, YD, 4>(a, waves, s));
 }
 
 hipError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int x_bits, int y_dt, hipStream_t s) {

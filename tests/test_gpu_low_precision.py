@@ -5,14 +5,17 @@ step.
 Error bounds as in test_gpu_ops.py: u = 2^-24 is half an fp32 step; a sum of n fp32
 terms in any order is off by at most n u times the sum of the magnitudes; a result
 rounded once to type t by half a step more."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
 
 import adamw_optimizer_step_amd as ma
+from adamw_optimizer_step_amd import _lib as L
 from gpu_util import need_gpu, say, to_np
 from oracle import train_ops as T
-from test_gpu_ops import BF16, DEPTH, DEV, F32, NORM_SHAPES, U, close, f64, guards, rand, view
+from test_gpu_ops import BF16, DEPTH, DEV, F32, NORM_SHAPES, U, close, f64, guards, half, rand, view
 
 pytestmark = pytest.mark.gpu
 
@@ -355,6 +358,75 @@ def test_product_keeps_nonfinite_values_in_their_row_and_column(rows, bits):
     got = ma.mx4_matmul(x, ma.mx4_pack(wv), dtype=F32)
     bad = torch.zeros(rows, outs, dtype=torch.bool, device=DEV)
     bad[3], bad[:, 7], bad[:, 299] = True, True, True
+    assert torch.equal(torch.isnan(got), bad) and bool(torch.isfinite(got[~bad]).all())
+
+
+def plan(rows, outs, ins, bits):
+    e, n = C.c_int32(-1), C.c_int32(-1)
+    assert L.lib().ma_test_mx4_matmul_plan(rows, outs, ins, bits, C.byref(e), C.byref(n)) == 0
+    return e.value, n.value
+
+
+# (sizes, the output tile's edge, whether the columns are split, whether a block works on several tiles): every form,
+# k-tiles fewer than are kept ahead and more, ragged edges, several tiles after one another
+FORMS = [(1300, 1700, 900, 128, False, False), (2100, 2100, 300, 128, False, False), (5000, 5003, 100, 128, False, True), (9001, 4100, 260, 128, False, True),
+         (4400, 2101, 390, 128, False, True), (900, 521, 20000, 128, True, False), (300, 700, 16000, 128, True, False), (6000, 9001, 700, 256, False, True),
+         (2000, 2050, 9000, 256, True, False), (2049, 2047, 12000, 256, True, False), (7000, 7101, 1900, 256, False, True), (4401, 1857, 16761, 256, True, True)]
+
+
+@pytest.mark.parametrize("rows,outs,ins,edge,split,several", FORMS)
+@pytest.mark.parametrize("bits,yd,acc,off", [(4, BF16, False, 1), (4, F32, True, 3), (8, BF16, True, 0), (8, F32, False, 1)])
+def test_product_of_every_form(rows, outs, ins, edge, split, several, bits, yd, acc, off):
+    say("mx4_matmul form", rows, outs, ins, edge, split, several, bits, yd, acc, off)
+    e, n = plan(rows, outs, ins, bits)
+    jobs = -(-rows // e) * -(-outs // e) * n
+    assert (e, n > 1, jobs > (512 if e == 128 else 256)) == (edge, split, several)
+    g = torch.Generator(device=DEV).manual_seed(155)
+    x = torch.randn(rows, ins, generator=g, device=DEV) * torch.exp2(torch.randint(-3, 4, (rows, 1), generator=g, device=DEV).float())
+    w = ma.mx4_pack(torch.randn(outs, ins, generator=g, device=DEV) * 0.05)
+    x = ma.mx4_pack(x) if bits == 4 else ma.act_pack(x)
+    xn = (ma.mx4_unpack(x, dtype=F32) if bits == 4 else ma.act_unpack(x, dtype=F32)).double()
+    wn = ma.mx4_unpack(w, dtype=F32).double()
+    y0 = torch.randn(rows, outs, generator=g, device=DEV).to(yd)
+    want, mag = torch.mm(xn, wn.t()), torch.mm(xn.abs(), wn.abs().t())
+    yb, yv = view(y0, off)
+    ma.mx4_matmul(x, w, out=yv, accumulate=acc)
+    tol = product_tol(mag, ins)
+    if acc:
+        want, tol = want + y0.double(), tol + U * (y0.double().abs() + mag)
+    bound = tol * (1 + half(yd)) + half(yd) * want.abs() + 2.0 ** -126
+    assert bool(((yv.double() - want).abs() <= bound).all())
+    assert guards(yb, rows * outs, off)
+    again = y0.clone()
+    ma.mx4_matmul(x, w, out=again, accumulate=acc)
+    assert torch.equal(again, yv)
+
+
+@pytest.mark.parametrize("rows,outs,ins", [f[:3] for f in FORMS])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_product_of_whole_numbers_is_exact_in_every_form(rows, outs, ins, bits):
+    say("mx4_matmul form, whole numbers", rows, outs, ins, bits)
+    g = torch.Generator(device=DEV).manual_seed(165)
+    table = torch.tensor([0, 1, 2, 3, 4, 6, -1, -2, -3, -4, -6], dtype=F32, device=DEV)
+    xv, wv = (table[torch.randint(0, 11, (n, ins), generator=g, device=DEV)] for n in (rows, outs))
+    xv[:, ::32], wv[:, ::32] = 6, -6      # every block's exponent 0
+    w = ma.mx4_pack(wv)
+    x = ma.mx4_pack(xv) if bits == 4 else ma.act_pack(xv)
+    want = torch.mm(xv.double(), wv.double().t())
+    assert torch.equal(ma.mx4_matmul(x, w, dtype=F32).double(), want)
+    assert torch.equal(ma.mx4_matmul(x, w, out=torch.full((rows, outs), 5.0, device=DEV), accumulate=True).double(), want + 5)
+
+
+@pytest.mark.parametrize("rows,outs,ins", [(1300, 1700, 900), (900, 521, 20000), (3000, 6001, 700), (2000, 2050, 9000)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_product_keeps_nonfinite_values_apart_in_every_form(rows, outs, ins, bits):
+    g = torch.Generator(device=DEV).manual_seed(175)
+    xv, wv = (torch.randn(n, ins, generator=g, device=DEV) for n in (rows, outs))
+    xv[rows - 1, ins - 1], xv[130, 0], wv[7, 5], wv[outs - 1, ins - 1] = float("nan"), float("nan"), float("inf"), float("nan")
+    x = ma.mx4_pack(xv) if bits == 4 else ma.act_pack(xv)
+    got = ma.mx4_matmul(x, ma.mx4_pack(wv))
+    bad = torch.zeros(rows, outs, dtype=torch.bool, device=DEV)
+    bad[rows - 1], bad[130], bad[:, 7], bad[:, outs - 1] = True, True, True, True
     assert torch.equal(torch.isnan(got), bad) and bool(torch.isfinite(got[~bad]).all())
 
 

@@ -1,6 +1,7 @@
 """Root-mean-square norm, 4-bit matrices and their product without a GPU: every
 entry point rejects bad arguments before any launch, and the binding rejects
 wrong types, shapes, strides and host tensors."""
+import ctypes as C
 import os
 
 import pytest
@@ -92,6 +93,35 @@ def test_workspace_sizes():
     for cols in (1, 700, 1500, 2047, 4096, 8192, 16384):
         sizes = [ma.rmsnorm_workspace_size(rows, cols) for rows in [*range(0, 3000, 7), 4096, 5000, 20000, 49152, 1 << 20]]
         assert sizes == sorted(sizes)
+
+
+def plan(rows, outs, ins, bits):
+    e, s = C.c_int32(-1), C.c_int32(-1)
+    assert L.lib().ma_test_mx4_matmul_plan(rows, outs, ins, bits, C.byref(e), C.byref(s)) == 0
+    return e.value, s.value
+
+
+def test_product_plan_query():
+    """The query says what the workspace sizes say, and rejects what they reject."""
+    for sizes in ((0, 4, 4), (1, 1, 1), (1, 16384, 4096), (129, 1003, 333), (12288, 16384, 4096), (900, 521, 20000), (2000, 2050, 9000), (1 << 24, 1, 1 << 12),
+                  (1, 1 << 23, 1 << 13), (1 << 24, 4096, 1)):
+        for bits in (4, 8):
+            edge, splits = plan(*sizes, bits)
+            assert edge in (0, 128, 256) and 1 <= splits <= -(-sizes[2] // 128) and (edge or splits == 1)
+            assert ma.mx4_matmul_workspace_size(*sizes, bits) == (0 if splits == 1 else splits * -(-sizes[0] * sizes[1] // 64) * 64 * 4)
+    assert plan(1, 16384, 4096, 8) == (0, 1) and plan(12288, 16384, 4096, 4) == (256, 1) and plan(900, 521, 20000, 4)[1] > 1
+    e, f = C.c_int32(), L.lib().ma_test_mx4_matmul_plan
+    assert f(-1, 4, 4, 4, C.byref(e), C.byref(e)) == INV and f(4, 0, 4, 4, C.byref(e), C.byref(e)) == INV and f(4, 4, 4, 5, C.byref(e), C.byref(e)) == UNS
+    assert f(4, 4, 4, 4, None, C.byref(e)) == INV and f(4, 4, 4, 4, C.byref(e), None) == INV
+
+
+def test_a_product_that_needs_a_workspace_rejects_a_small_one():
+    need = ma.mx4_matmul_workspace_size(900, 521, 20000)
+    assert need > 0
+    for kw in (dict(workspace=None), dict(workspace_bytes=need - 1), dict(workspace=at(5) + 64)):
+        assert call(M, rows=900, outs=521, ins=20000, **kw) == WS
+    assert call(M, rows=900, outs=521, ins=20000, workspace=at(4) + 256) == INV
+    assert call(M, rows=900, outs=521, ins=20000, workspace=at(2)) == INV
 
 
 def test_binding_rejects_wrong_tensors():
