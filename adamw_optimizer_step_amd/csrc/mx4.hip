@@ -5,36 +5,46 @@
 
 namespace ma {
 
-// Packing along the rows: 16 lanes hold a k-tile of 128 columns of one row, 8 values
-// per lane, 4 lanes a block of 32; 4 k-tiles per group of lanes in flight.
+// Packing along the rows: 16 lanes hold a k-tile of 128 columns of one row, 8
+// values per lane, 4 lanes a block of 32. A block of threads takes 16 rows and up to 4 k-tiles of
+// each, all in flight: 1 KB of a row of bf16 and, for each k-tile, 64 bytes of scales at once
+// (of narrower matrices, more rows).
 constexpr int kMx4Unroll = 4;
 
+struct Mx4Place {
+  int64_t row;
+  int t;
+  bool in;
+};
+// the place of part u of this thread block's 16 groups of lanes; log2t: 4 >> log2t rows apart
+__device__ __forceinline__ Mx4Place mx4_place(const Mx4Args& a, int u, int kt, int log2t) {
+  const int per = (kt + (1 << log2t) - 1) >> log2t;   // thread blocks along a row
+  const uint32_t block = blockIdx.x / (uint32_t)per, at = blockIdx.x - block * per;
+  Mx4Place p;
+  p.row = (int64_t)block * (16 * kMx4Unroll >> log2t) + (u >> log2t) * 16 + threadIdx.x / 16;
+  p.t = (int)(at << log2t) + (u & ((1 << log2t) - 1));
+  p.in = p.row < a.rows && p.t < kt;
+  return p;
+}
+static int mx4_log2t(int64_t kt) { return kt >= 3 ? 2 : (kt == 2 ? 1 : 0); }
+
 template <int XD, bool NT>
-__global__ void __launch_bounds__(256) k_mx4_pack(const Mx4Args a) {
-  const int lane = threadIdx.x & 15;
-  const int64_t kt = mx4_tiles(a.cols), total = a.rows * kt;
-  const int64_t b0 = (int64_t)blockIdx.x * (16 * kMx4Unroll) + threadIdx.x / 16;
+__global__ void __launch_bounds__(256) k_mx4_pack(const Mx4Args a, int log2t) {
+  const int lane = threadIdx.x & 15, kt = (int)mx4_tiles(a.cols);
   Raw8<XD> raw[kMx4Unroll];
-  int col[kMx4Unroll];
 #pragma unroll
   for (int u = 0; u < kMx4Unroll; ++u) {
-    const int64_t b = b0 + u * 16;
+    const Mx4Place p = mx4_place(a, u, kt, log2t);
+    const int col = p.t * kMx4Tile + lane * 8;
     raw[u] = raw_zero<XD>();
-    col[u] = 0;
-    if (b < total) {
-      const uint32_t row = (uint32_t)b / (uint32_t)kt;   // at most 2^29 k-tiles
-      const int at = (int)((uint32_t)b - row * (uint32_t)kt) * kMx4Tile + lane * 8;
-      if (at < a.cols) {
-        raw[u] = raw_load_row<XD, NT>(elem_ptr<XD>(a.x, (int64_t)row * a.cols), at, a.cols);
-        col[u] = at;
-      }
-    }
+    if (p.in && col < a.cols) raw[u] = raw_load_row<XD, NT>(elem_ptr<XD>(a.x, p.row * a.cols), col, a.cols);
   }
 #pragma unroll
   for (int u = 0; u < kMx4Unroll; ++u) {
-    const int64_t b = b0 + u * 16;
+    const Mx4Place p = mx4_place(a, u, kt, log2t);
+    const int col = p.t * kMx4Tile + lane * 8;
     float v[8];
-    raw_f32_row<XD>(raw[u], col[u], a.cols, v);
+    raw_f32_row<XD>(raw[u], col < a.cols ? col : 0, a.cols, v);
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -45,13 +55,14 @@ __global__ void __launch_bounds__(256) k_mx4_pack(const Mx4Args a) {
     m = m > o ? m : o;
     o = dpp<kDppPair>(m);
     m = m > o ? m : o;
-    if (b >= total) continue;
     const uint32_t byte = mx4_scale_byte(m);
-    reinterpret_cast<uint32_t*>(a.q)[b * 16 + lane] = mx4_encode(v, byte);
-    if ((lane & 3) == 0) {
-      const uint32_t row = (uint32_t)b / (uint32_t)kt, t = (uint32_t)b - row * (uint32_t)kt;
-      a.scale[((int64_t)t * a.rows + row) * 4 + lane / 4] = (uint8_t)byte;
-    }
+    // the k-tile's 4 bytes as one word, in every lane of its 16
+    uint32_t word = byte << (8 * (lane / 4));
+    word |= dpp<kDppHalfMirror>(word);
+    word |= dpp<kDppMirror>(word);
+    if (!p.in) continue;
+    reinterpret_cast<uint32_t*>(a.q)[(p.row * kt + p.t) * 16 + lane] = mx4_encode(v, byte);
+    if (lane == 0) reinterpret_cast<uint32_t*>(a.scale)[(int64_t)p.t * a.rows + p.row] = word;
   }
 }
 
@@ -60,14 +71,12 @@ __global__ void __launch_bounds__(256) k_mx4_pack(const Mx4Args a) {
 // wave's 8 groups of them 8 blocks of rows: 256 rows become 128 bytes of each packed
 // row, loaded and stored in whole lines without LDS.
 template <int XD>
-__global__ void __launch_bounds__(256) k_mx4_pack_t(const Mx4Args a) {
+__global__ void __launch_bounds__(64) k_mx4_pack_t(const Mx4Args a) {
   typedef typename U16<XD>::T V;
   constexpr int E = 16 / elem_bytes<XD>();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t bands = (a.rows + 255) / 256, strips = (a.cols + 8 * E - 1) / (8 * E);
-  const int64_t job = (int64_t)blockIdx.x * 4 + wave;
-  if (job >= bands * strips) return;
-  const int64_t r0 = job / strips * 256 + (lane >> 3) * 32;
+  const int lane = threadIdx.x;
+  const int64_t strips = (a.cols + 8 * E - 1) / (8 * E);
+  const int64_t job = blockIdx.x, r0 = job / strips * 256 + (lane >> 3) * 32;
   const int64_t at = (job % strips) * (8 * E) + (lane & 7) * E;
   const int64_t kt = mx4_tiles(a.rows), padded = kt * kMx4Tile;
   if (at >= a.cols || r0 >= padded) return;
@@ -117,6 +126,7 @@ __global__ void __launch_bounds__(256) k_mx4_pack_t(const Mx4Args a) {
   }
 }
 
+// Unpacking: the same lanes, k-tiles one after the other along the rows, as what it writes is the most.
 template <int OD, bool NT>
 __global__ void __launch_bounds__(256) k_mx4_unpack(const Mx4Args a) {
   const int lane = threadIdx.x & 15;
@@ -128,7 +138,7 @@ __global__ void __launch_bounds__(256) k_mx4_unpack(const Mx4Args a) {
     const int64_t b = b0 + u * 16;
     q[u] = s[u] = 0;
     if (b < total) {
-      const uint32_t row = (uint32_t)b / (uint32_t)kt, t = (uint32_t)b - row * (uint32_t)kt;
+      const uint32_t row = (uint32_t)b / (uint32_t)kt, t = (uint32_t)b - row * (uint32_t)kt;   // at most 2^29 k-tiles
       q[u] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(a.q) + b * 16 + lane);
       s[u] = a.scale[((int64_t)t * a.rows + row) * 4 + lane / 4];
     }
@@ -147,30 +157,33 @@ __global__ void __launch_bounds__(256) k_mx4_unpack(const Mx4Args a) {
 }
 
 static dim3 mx4_grid(const Mx4Args& a) {
-  const int64_t per = 16 * kMx4Unroll;
-  return dim3((unsigned)((a.rows * mx4_tiles(a.cols) + per - 1) / per));
+  const int64_t kt = mx4_tiles(a.cols), log2t = mx4_log2t(kt), rows = 16 * kMx4Unroll >> log2t;
+  return dim3((unsigned)((a.rows + rows - 1) / rows * ((kt + (1 << log2t) - 1) >> log2t)));
 }
 
 hipError_t launch_mx4_pack(const Mx4Args& a, int x_dt, bool transpose, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
-  auto go = [&](auto k, dim3 grid) { hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a); };
   const bool f32 = x_dt == DT_F32;
   if (transpose) {
-    const int64_t strip = f32 ? 32 : 64, jobs = (a.rows + 255) / 256 * ((a.cols + strip - 1) / strip);
-    const dim3 grid((unsigned)((jobs + 3) / 4));
-    f32 ? go(k_mx4_pack_t<DT_F32>, grid) : go(k_mx4_pack_t<DT_BF16>, grid);
+    const int64_t strip = f32 ? 32 : 64;
+    const dim3 grid((unsigned)((a.rows + 255) / 256 * ((a.cols + strip - 1) / strip)));
+    if (f32) hipLaunchKernelGGL(k_mx4_pack_t<DT_F32>, grid, dim3(64), 0, s, a);
+    else hipLaunchKernelGGL(k_mx4_pack_t<DT_BF16>, grid, dim3(64), 0, s, a);
     return hipGetLastError();
   }
   const bool stream = a.rows * a.cols * (f32 ? 4 : 2) > kStreamBytes;
-  if (f32) stream ? go(k_mx4_pack<DT_F32, true>, mx4_grid(a)) : go(k_mx4_pack<DT_F32, false>, mx4_grid(a));
-  else stream ? go(k_mx4_pack<DT_BF16, true>, mx4_grid(a)) : go(k_mx4_pack<DT_BF16, false>, mx4_grid(a));
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, mx4_grid(a), dim3(256), 0, s, a, mx4_log2t(mx4_tiles(a.cols))); };
+  if (f32) stream ? go(k_mx4_pack<DT_F32, true>) : go(k_mx4_pack<DT_F32, false>);
+  else stream ? go(k_mx4_pack<DT_BF16, true>) : go(k_mx4_pack<DT_BF16, false>);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_unpack(const Mx4Args& a, int out_dt, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
   const bool stream = a.rows * a.cols * (out_dt == DT_F32 ? 4 : 2) > kStreamBytes;
-  auto go = [&](auto k) { hipLaunchKernelGGL(k, mx4_grid(a), dim3(256), 0, s, a); };
+  const int64_t per = 16 * kMx4Unroll;
+  const dim3 grid((unsigned)((a.rows * mx4_tiles(a.cols) + per - 1) / per));
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a); };
   if (out_dt == DT_F32) stream ? go(k_mx4_unpack<DT_F32, true>) : go(k_mx4_unpack<DT_F32, false>);
   else stream ? go(k_mx4_unpack<DT_BF16, true>) : go(k_mx4_unpack<DT_BF16, false>);
   return hipGetLastError();

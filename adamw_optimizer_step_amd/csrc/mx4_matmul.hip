@@ -29,7 +29,7 @@ __device__ __forceinline__ f32x4_t mx_mfma16(const i32x8_t& w, const i32x8_t& x,
 // further: so the instruction pairs them with 4-bit ones). Rows past the end are read
 // from inside the matrix; their results are not stored.
 template <int XB, int YD, int MB>
-__global__ void __launch_bounds__(1024) k_mx4_rows(const Mx4MatmulArgs a) {
+__global__ void __launch_bounds__(512) k_mx4_rows(const Mx4MatmulArgs a) {
   extern __shared__ float join[];   // [waves][MB][64][4]
   constexpr int U = MB == 1 ? 4 : 2, XV = XB == 8 ? 2 : 1;   // k-tiles in flight
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -255,7 +255,9 @@ struct Mx4Job {
 // The k-tiles of one output tile follow on those of the one before: its first ones are copied,
 // and its first fragments read, before the results are stored, and the stores end while it is
 // worked on. Results go from the registers to memory, without LDS or a barrier.
-template <typename TL, int YD>
+// ADDS: results are added to y (whole sums only), in kernels of their own: in one with the others,
+// 12288 x (16384 x 4096) of 4 bits takes 569 us, else 523 on the same card.
+template <typename TL, int YD, bool ADDS>
 __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(const Mx4MatmulArgs a) {
   constexpr int XB = TL::XB, FM = TL::FM, FN = TL::FN, S = TL::STAGES;
   constexpr int XC = TL::XR / 16;   // chunks of a row
@@ -421,8 +423,36 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       constexpr bool ADD = decltype(adds)::value, PAIRS = OD == DT_BF16 && !ADD, NT = decltype(past)::value;
       constexpr int E = PAIRS ? 8 : 4, W = PAIRS ? 4 : 2;   // outputs per lane; blocks that are side by side
       unsigned char* const base = a.splits > 1 ? elem_ptr<OD>(a.partial, j.split * mx4_partial(a.rows, a.outs)) : reinterpret_cast<unsigned char*>(a.y);
+      // what is added to, 16 rows ahead in place of those that are done: loaded where it is needed,
+      // each is a memory's latency (24576 x (2048 x 8192) of 4 bits onto fp32 314 us, so 283)
+      Raw4<OD> old[ADD ? FN : 1];
+      auto load = [&](int i, int b) __attribute__((always_inline)) {
+        if constexpr (ADD) {
+          const int n = at_n + b * 16 + (l16 >> 3) * 16 + g * 4;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+          for (int h = 0; h < 2; ++h) {
+            const int64_t m = (int64_t)at_m + i * 16 + h * 8;
+            Raw4<OD>& r = old[b + h];
+            r = quad_zero<OD>();
+            if (m >= a.rows || n >= a.outs) continue;
+            const unsigned char* const row = base + m * a.outs * elem_bytes<OD>();
+            if (n + 4 <= a.outs) {
+              r.u = *reinterpret_cast<const typename Quad<OD>::T*>(row + (int64_t)n * elem_bytes<OD>());
+            } else {
+#pragma unroll
+              for (int e = 0; e < 3; ++e) {
+                if (n + e >= a.outs) continue;
+                if constexpr (OD == DT_BF16) r.u[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[n + e] << (16 * (e % 2));
+                else r.u[e] = reinterpret_cast<const uint32_t*>(row)[n + e];
+              }
+            }
+          }
+        }
+      };
+#pragma unroll
+      for (int b = 0; ADD && b < FN; b += 2) load(0, b);
+      each<FM>([&](auto number) __attribute__((always_inline)) {
+        constexpr int i = decltype(number)::value;
 #pragma unroll
         for (int b = 0; b < FN; b += 4) settled<ACC_A>(acc[i][b], acc[i][b + 1], acc[i][b + 2], acc[i][b + 3]);
 #pragma unroll
@@ -458,35 +488,32 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(part[h][e]);
               if constexpr (ADD) {
-                float old[4];
-                if (n + 4 <= a.outs) {
-                  Raw4<OD> r;
-                  r.u = *reinterpret_cast<const typename Quad<OD>::T*>(row + (int64_t)n * elem_bytes<OD>());
-                  quad_f32<OD>(r, 0, 4, old);
-                } else {
+                float o[4];
+                quad_f32<OD>(old[b + h], 0, 4, o);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) old[e] = n + e < a.outs ? load1<OD>(row, n + e) : 0.0f;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(old[e], v[e]);
+                for (int e = 0; e < 4; ++e) v[e] = __fadd_rn(o[e], v[e]);
               }
               quad_store_row<OD, NT>(row, n, a.outs, v);
             }
           }
+          if constexpr (ADD && i + 1 < FM) load(i + 1, b);
         }
 #pragma unroll
         for (int b = 0; b < FN; ++b) acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
     };
     typedef std::integral_constant<int, DT_F32> F;
     typedef std::integral_constant<int, YD> Y;
     typedef std::integral_constant<bool, true> Yes;
     typedef std::integral_constant<bool, false> No;
-    if (a.splits > 1) put(F(), No(), No());
-    else if (a.accumulate) put(Y(), Yes(), No());
-    else if (a.stream) put(Y(), No(), Yes());
-    else put(Y(), No(), No());
+    if constexpr (ADDS) {
+      put(Y(), Yes(), No());
+    } else {
+      if (a.splits > 1) put(F(), No(), No());
+      else if (a.stream) put(Y(), No(), Yes());
+      else put(Y(), No(), No());
+    }
   };
 
   copies_of(job_at(job));
@@ -566,7 +593,9 @@ __global__ void __launch_bounds__(256) k_mx4_join(const Mx4MatmulArgs a) {
   }
 }
 
-// Few rows: blocks of 16, 32 or 64 rows, and waves per block: 16 per CU where that leaves each 2 k-tiles.
+// Few rows: blocks of 16, 32 or 64 rows, and waves per block: 8 of them, fewer where blocks * waves would be
+// beyond 32 per CU or a wave would have less than 2 k-tiles. (1 x (4096 x 4096) of 4 bits 4.5 us with 8 waves,
+// 4.8 with 16; 1 x (4096 x 16384) 8.8 and 9.6; 1 x (16384 x 4096) 8.7 with 8 and 9.0 with 4.)
 static int mx4_rows_mb(int64_t rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
 static int64_t mx4_rows_blocks(int64_t rows, int64_t outs) {
   const int64_t m = 16 * mx4_rows_mb(rows);
@@ -575,7 +604,7 @@ static int64_t mx4_rows_blocks(int64_t rows, int64_t outs) {
 static int mx4_rows_waves(int64_t rows, int64_t outs, int64_t ins) {
   const int64_t blocks = mx4_rows_blocks(rows, outs), kt = mx4_tiles(ins);
   int waves = 1;
-  while (waves < 16 && blocks * waves < 4096 && kt >= 4 * waves) waves *= 2;
+  while (waves < 8 && blocks * waves < 8192 && kt >= 4 * waves) waves *= 2;
   return waves;
 }
 
@@ -621,7 +650,9 @@ template <typename TL, int YD>
 static hipError_t mx4_tile(const Mx4MatmulArgs& a, hipStream_t s) {
   const int64_t jobs = ((a.rows + TL::BM - 1) / TL::BM) * ((a.outs + TL::BN - 1) / TL::BN) * a.splits;
   const int64_t want = (jobs + 7) / 8 * 8, most = 256 * TL::BLOCKS;   // resident blocks
-  hipLaunchKernelGGL((k_mx4_tile<TL, YD>), dim3((unsigned)(want < most ? want : most)), dim3(TL::NT), 0, s, a);
+  const dim3 grid((unsigned)(want < most ? want : most));
+  if (a.accumulate && a.splits == 1) hipLaunchKernelGGL((k_mx4_tile<TL, YD, true>), grid, dim3(TL::NT), 0, s, a);
+  else hipLaunchKernelGGL((k_mx4_tile<TL, YD, false>), grid, dim3(TL::NT), 0, s, a);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || a.splits == 1) return err;
   hipLaunchKernelGGL((k_mx4_join<YD>), dim3((unsigned)((a.rows * a.outs + 1023) / 1024)), dim3(256), 0, s, a);
