@@ -430,6 +430,42 @@ def test_product_keeps_nonfinite_values_apart_in_every_form(rows, outs, ins, bit
     assert torch.equal(torch.isnan(got), bad) and bool(torch.isfinite(got[~bad]).all())
 
 
+def beside_large(rows, outs, ins):
+    """8-bit rows whose small values stand beside large ones in every 8 of them, and weights: all products are multiples of
+    2^-10, and only three columns of the largest values have weights, so that sums stay below 2^14."""
+    g = torch.Generator(device=DEV).manual_seed(181)
+    xv = torch.randint(-15, 16, (rows, ins), generator=g, device=DEV).float() * 2.0 ** -9
+    middle = torch.randint(-15, 16, (rows, ins), generator=g, device=DEV).float() * 2.0 ** -2
+    xv = torch.where(torch.rand(rows, ins, generator=g, device=DEV) < 0.1, middle, xv)
+    table = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.5, -1, -1.5, -2, -3, -4, -6], device=DEV)
+    wv = table[torch.randint(0, 15, (outs, ins), generator=g, device=DEV)]
+    wv[:, ::32] = 6                                        # every block's exponent 0
+    at = torch.arange(0, ins, 128, device=DEV)
+    large = torch.minimum(at + at // 128 * 37 % 128, torch.tensor(ins - 1, device=DEV))
+    xv[:, large] = 448.0 * (1 - 2 * torch.randint(0, 2, (rows, large.numel()), generator=g, device=DEV).float())
+    wv[:, large] = 0
+    wv[:, large[::max(1, large.numel() // 3)][:3]] = 4
+    x, w = ma.act_pack(xv), ma.mx4_pack(wv)
+    assert torch.equal(ma.act_unpack(x, dtype=F32), xv) and torch.equal(ma.mx4_unpack(w, dtype=F32), wv)
+    return x, w, xv.double(), wv.double()
+
+
+@pytest.mark.parametrize("rows,outs,ins", [(1, 40, 300), (3, 17, 100), (20, 64, 4000), (60, 64, 700), (200, 300, 1030)] + [f[:3] for f in FORMS])
+def test_product_of_8_bit_rows_keeps_small_products_beside_large_ones(rows, outs, ins):
+    """All sums are whole multiples of 2^-10 below 2^14: fp32 results have every bit. A bf16 result may lose, of 7
+    products of 8, less than 2^-13 of the largest one's power of two, beside its own rounding."""
+    say("mx4_matmul, small beside large", rows, outs, ins)
+    x, w, xv, wv = beside_large(rows, outs, ins)
+    want = torch.mm(xv, wv.t())
+    assert torch.equal(ma.mx4_matmul(x, w, dtype=F32).double(), want)
+    assert torch.equal(ma.mx4_matmul(x, w, out=torch.full((rows, outs), 0.25, device=DEV), accumulate=True).double(), want + 0.25)
+    pad = torch.nn.functional.pad
+    most = torch.mm(pad(xv, (0, -ins % 8)).abs().view(rows, -1, 8).amax(2), pad(wv, (0, -ins % 8)).abs().view(outs, -1, 8).amax(2).t())
+    got = ma.mx4_matmul(x, w).double()
+    cut = 7 * 2.0 ** -13 * most + product_tol(torch.mm(xv.abs(), wv.abs().t()), ins)
+    assert bool(((got - want).abs() <= cut * (1 + half(BF16)) + half(BF16) * want.abs()).all())
+
+
 def test_product_shapes_and_defaults():
     x, w = ma.mx4_pack(rand((4, 40), 190)), ma.mx4_pack(rand((6, 40), 191))
     y = ma.mx4_matmul(x, w)
