@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       const int r = (wave * TL::NWT + q) * 16 + lane / 4, c = (lane % 4) ^ spread<4>(r);
       woff[q] = (uint32_t)(r < nlast ? r : nlast) * (uint32_t)(kt * TL::WR) + (uint32_t)c * 16;
     }
-    const int r = wave * 32 + (lane & 31);
+    // scales: those of rows r, r + 16, r + 32 and r + 48 lie side by side
+    const int r = wave / 2 * 64 + lane % 4 * 16 + wave % 2 * 8 + (lane & 31) / 4;
     sxoff = (uint32_t)(r < mlast ? r : mlast) * (XB == 8 ? (uint32_t)kt : 4u);
     swoff = (uint32_t)(r < nlast ? r : nlast) * 4u;
     xq = a.xq + ((int64_t)j.m0 * kt + j.v0) * TL::XR;
@@ -379,9 +380,8 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
   const int swx = spread<XC>(l16), sww = spread<4>(l16);
   const int xat = (wm * TL::WTM + l16) * TL::XR, wat = TL::W_AT + (wn * TL::WTN + l16) * TL::WR + ((g ^ sww) << 4);
   const int xat0 = xat + ((g ^ swx) << 4), xat1 = xat + (((4 + g) ^ swx) << 4);
-  const int sxat = TL::S_AT + (wm * TL::WTM + l16) * 4, swat = TL::S_AT + (TL::BM + wn * TL::WTN + l16) * 4;
+  const int sxat = TL::S_AT + wm * TL::WTM * 4 + l16 * 16, swat = TL::S_AT + (TL::BM + wn * TL::WTN) * 4 + l16 * 16;
   typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
-  typedef __attribute__((address_space(3))) int lds_int_t;
   auto read_x = [&](lds_u8_t* st, int i) __attribute__((always_inline)) {
     const u32x4_t lo = *(lds_u32x4_t*)(st + xat0 + i * 16 * TL::XR);
     if constexpr (XB == 8) {
@@ -391,15 +391,22 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       fx[i] = lo;
     }
   };
-  auto read_sx = [&](lds_u8_t* st, int i) __attribute__((always_inline)) { rx[i] = *(lds_int_t*)(st + sxat + i * 64); };
-  auto read_w = [&](lds_u8_t* st, int j) __attribute__((always_inline)) {
-    fw[j] = *(lds_u32x4_t*)(st + wat + j * 16 * TL::WR);
-    rw[j] = *(lds_int_t*)(st + swat + j * 64);
+  auto read_w = [&](lds_u8_t* st, int j) __attribute__((always_inline)) { fw[j] = *(lds_u32x4_t*)(st + wat + j * 16 * TL::WR); };
+  // the scales of 4 blocks at once: a quarter of the reads (12288 x (4096 x 16384) of 8 bits onto fp32 1144 -> 1119 us)
+  auto read_sx = [&](lds_u8_t* st, int four) __attribute__((always_inline)) {
+    const u32x4_t v = *(lds_u32x4_t*)(st + sxat + four * 256);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rx[four * 4 + i] = (int)v[i];
   };
-  constexpr int MM = FM * FN, HALF = MM / 2, LATER = 2 * (FM - 2);   // LATER: reads of x and scales in the first half
+  auto read_sw = [&](lds_u8_t* st) __attribute__((always_inline)) {
+    const u32x4_t v = *(lds_u32x4_t*)(st + swat);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rw[j] = (int)v[j];
+  };
+  constexpr int MM = FM * FN, HALF = MM / 2, LATER = FM - 2;   // LATER: reads of x in the first half
   // copies after every SPACE-th MFMA from the barrier on
   constexpr int SPACE = MM / TL::COPIES;
-  static_assert(SPACE >= 1 && FM >= 4 && FM % 4 == 0 && LATER <= HALF * 3 / 4, "copies and reads fit between the MFMAs");
+  static_assert(SPACE >= 1 && (FM == 4 || FM == 8) && FN == 4 && LATER <= HALF * 3 / 4, "copies and reads fit between the MFMAs");
 
   // MFMA k of a k-tile, from the scales' words on; EXACT: two of them, x block by x block, the large
   // parts of x for all of w's blocks and then the others
@@ -410,13 +417,14 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
     if constexpr (EXACT) {
       constexpr int i = k / FN, part = k % FN / (FN / 2), j0 = k % (FN / 2) * 2;
       if constexpr (j0 == 0 && part == 0) {
+        sx[0] = rx[i];
         large = mx_large(fx[i]);
         fx[i] = fx[i] ^ large;
       }
       each<2>([&](auto other) __attribute__((always_inline)) {
         constexpr int j = j0 + decltype(other)::value;
         if constexpr (i == 0 && part == 0) sw[j] = (int)((unsigned)rw[j] >> (8 * g));
-        mx_mfma16_into<XB, ACC_A, (i == 0 && part == 0) || j == 0>(acc[i][j], fw[j], part == 0 ? large : fx[i], sw[j], rx[i]);
+        mx_mfma16_into<XB, ACC_A, (i == 0 && part == 0) || j == 0>(acc[i][j], fw[j], part == 0 ? large : fx[i], sw[j], sx[0]);
       });
     } else {
       constexpr int i = k / (2 * FN) * 2 + k % 2, j = k % (2 * FN) / 2;
@@ -433,11 +441,9 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       step(number);
       each<LATER>([&](auto n) __attribute__((always_inline)) {
         constexpr int b = decltype(n)::value;
-        if constexpr (b * (HALF * 3 / 4) / LATER == k) {
-          if constexpr (b % 2 == 0) read_x(cur, 2 + b / 2);
-          else read_sx(cur, 2 + b / 2);
-        }
+        if constexpr (b * (HALF * 3 / 4) / LATER == k) read_x(cur, 2 + b);
       });
+      if constexpr (FM == 8 && k == 1) read_sx(cur, 1);
       if constexpr (decltype(copies)::value && q % SPACE == 0 && q / SPACE < TL::COPIES) copy(to, q / SPACE);
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -448,7 +454,9 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       constexpr int q = decltype(number)::value, k = q + HALF;
       step(std::integral_constant<int, k>());
       if constexpr (q < 2) read_x(nxt, q);
-      else if constexpr (q < 4) read_sx(nxt, q - 2);
+      if constexpr (q == HALF - (EXACT ? 3 : 6)) read_sx(nxt, 0);   // the last blocks' are taken
+
+      if constexpr (q == HALF - 4) read_sw(nxt);
       if constexpr (EXACT && k >= MM - FN / 2) {
         read_w(nxt, k % (FN / 2) * 2);
         read_w(nxt, k % (FN / 2) * 2 + 1);
@@ -571,10 +579,9 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
   wait_vm<(S - 1) * TL::COPIES>();
   block_barrier();
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    read_x(lds, i);
-    read_sx(lds, i);
-  }
+  for (int i = 0; i < 2; ++i) read_x(lds, i);
+  read_sx(lds, 0);
+  read_sw(lds);
 #pragma unroll
   for (int j = 0; j < FN; ++j) read_w(lds, j);
   first(lds, lds, std::integral_constant<bool, false>());
