@@ -4,6 +4,10 @@
 // on the scaled matrix instructions of gfx950: 16 x 16 outputs and 128 k each, whose
 // operands are e2m1 or e4m3 values with a power of two for every 32 k, and whose
 // sums are fp32. Nothing is unpacked; products of held values are exact.
+//
+// Two kernels: few rows are bound by reading w (k_mx4_rows), many by the matrix instructions
+// (k_mx4_tile). On random data the chip's power holds those alone to 7.28 PFLOP/s for 4-bit
+// rows and 4.66 for 8-bit ones (9.6 and 5.0 on zeros); of 32 x 32 x 64 to 6.4 and 4.2.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -46,6 +50,8 @@ __device__ __forceinline__ i32x8_t mx_large(const i32x8_t& x) {
 // 32 values from 32 * (l / 16) (of 8-bit rows two times 16, from 16 * (l / 16) and 64
 // further: so the instruction pairs them with 4-bit ones). Rows past the end are read
 // from inside the matrix; their results are not stored.
+//   1 x (16384 x 4096) of 8 bits 9.9 us, 3.6 TB/s (4 k-tiles in flight; 8: no faster);
+//   129 x (1003 x 333) of 4 bits 6.2, a chain of two loads, the join and a store
 template <int XB, int YD, int MB>
 __global__ void __launch_bounds__(512) k_mx4_rows(const Mx4MatmulArgs a) {
   extern __shared__ float join[];   // [waves][MB][64][4]
@@ -181,33 +187,29 @@ __device__ __forceinline__ void block_barrier() {
 }
 
 // acc += w x, 16 x 16 outputs and 128 k, in place: from the builtin the compiler makes a new
-// accumulator each time, and moves them all. ACC_A: they are in the accumulation registers.
-// FRESH: a scale may have been computed by the instruction before, which needs two wait states.
-// Whoever reads acc otherwise calls settled() first.
+// accumulator each time, and moves them all. FRESH: w, x or a scale may have been computed by
+// the instruction before, which needs two wait states. Whoever reads acc otherwise calls
+// settled() first.
 template <int XB> struct MxRow { typedef u32x4_t T; };   // a lane's 32 values of x
 template <> struct MxRow<8> { typedef i32x8_t T; };
-template <int XB, bool ACC_A, bool FRESH>
+template <int XB, bool FRESH>
 __device__ __forceinline__ void mx_mfma16_into(f32x4_t& acc, u32x4_t w, typename MxRow<XB>::T x, int ws, int xs) {
 #if defined(__HIP_DEVICE_COMPILE__)   // (the host's pass knows other registers)
-#define MA_MFMA(wait, c, fmt)                                                                                                \
-  asm volatile(wait "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:" fmt : c(acc) : "v"(w), "v"(x), "v"(ws), "v"(xs))
+#define MA_MFMA(wait, fmt)                                                                                                   \
+  asm volatile(wait "v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:" fmt : "+v"(acc) : "v"(w), "v"(x), "v"(ws), "v"(xs))
   if constexpr (XB == 8) {
-    if constexpr (ACC_A) { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+a", "0"); else MA_MFMA("", "+a", "0"); }
-    else { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+v", "0"); else MA_MFMA("", "+v", "0"); }
+    if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "0"); else MA_MFMA("", "0");
   } else {
-    if constexpr (ACC_A) { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+a", "4"); else MA_MFMA("", "+a", "4"); }
-    else { if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "+v", "4"); else MA_MFMA("", "+v", "4"); }
+    if constexpr (FRESH) MA_MFMA("s_nop 1\n\t", "4"); else MA_MFMA("", "4");
   }
 #undef MA_MFMA
 #endif
 }
 
 // The MFMAs into these 4 accumulators are done: 16 passes and more have gone by.
-template <bool ACC_A>
 __device__ __forceinline__ void settled(f32x4_t& a, f32x4_t& b, f32x4_t& c, f32x4_t& d) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  if constexpr (ACC_A) asm volatile("s_nop 15\n\ts_nop 7" : "+a"(a), "+a"(b), "+a"(c), "+a"(d));
-  else asm volatile("s_nop 15\n\ts_nop 7" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+  asm volatile("s_nop 15\n\ts_nop 7" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
 #endif
 }
 
@@ -279,13 +281,19 @@ struct Mx4Job {
 // The k-tiles of one output tile follow on those of the one before: its first ones are copied,
 // and its first fragments read, before the results are stored, and the stores end while it is
 // worked on. Results go from the registers to memory, without LDS or a barrier.
+//
+// Measured: 12288 x (16384 x 4096) of 4 bits 447 us, 3.7 PFLOP/s, the matrix units busy for 44 % of the
+// cycles at 2.0 GHz; 12288 x (4096 x 16384) of 8 bits 583, 2.8, 69 % at 1.9 GHz. A k-tile of 256 x 256 takes 0.9 us
+// (4 bits; 1.35 of 8), of which the MFMAs alone are 0.61, the LDS reads alone 0.78, the copies alone 0.77; the
+// stores at a tile's end 5 us (bf16) to 15 (fp32), with all blocks' at the same time. Tried, and no faster: blocks
+// started at different times (+1 to +8 %), 4 waves of 128 x 128 (spills), 32 x 32 x 64 instructions,
+// copies in the k-tile's first part, branches between the MFMAs that spread the waves' copies.
 // ADDS: results are added to y (whole sums only), in kernels of their own: in one with the others,
 // 12288 x (16384 x 4096) of 4 bits takes 569 us, else 523 on the same card.
 template <typename TL, int YD, bool ADDS>
 __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(const Mx4MatmulArgs a) {
   constexpr int XB = TL::XB, FM = TL::FM, FN = TL::FN, S = TL::STAGES;
   constexpr int XC = TL::XR / 16;   // chunks of a row
-  constexpr bool ACC_A = FM * FN > 32;   // 256 accumulators per lane are all the accumulation registers
   __shared__ __attribute__((aligned(1024))) unsigned char smem[S * TL::STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WGN, wn = wave % TL::WGN, l16 = lane & 15, g = lane >> 4;
@@ -424,13 +432,13 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       each<2>([&](auto other) __attribute__((always_inline)) {
         constexpr int j = j0 + decltype(other)::value;
         if constexpr (i == 0 && part == 0) sw[j] = (int)((unsigned)rw[j] >> (8 * g));
-        mx_mfma16_into<XB, ACC_A, (i == 0 && part == 0) || j == 0>(acc[i][j], fw[j], part == 0 ? large : fx[i], sw[j], sx[0]);
+        mx_mfma16_into<XB, (i == 0 && part == 0) || j == 0>(acc[i][j], fw[j], part == 0 ? large : fx[i], sw[j], sx[0]);
       });
     } else {
       constexpr int i = k / (2 * FN) * 2 + k % 2, j = k % (2 * FN) / 2;
       if constexpr (i == 0) sw[j] = (int)((unsigned)rw[j] >> (8 * g));
       if constexpr (j == 0) sx[i % 2] = XB == 8 ? rx[i] : (int)((unsigned)rx[i] >> (8 * g));
-      mx_mfma16_into<XB, ACC_A, i == 0 || j == 0>(acc[i][j], fw[j], fx[i], sw[j], sx[i % 2]);
+      mx_mfma16_into<XB, i == 0 || j == 0>(acc[i][j], fw[j], fx[i], sw[j], sx[i % 2]);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -507,7 +515,7 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       each<FM>([&](auto number) __attribute__((always_inline)) {
         constexpr int i = decltype(number)::value;
 #pragma unroll
-        for (int b = 0; b < FN; b += 4) settled<ACC_A>(acc[i][b], acc[i][b + 1], acc[i][b + 2], acc[i][b + 3]);
+        for (int b = 0; b < FN; b += 4) settled(acc[i][b], acc[i][b + 1], acc[i][b + 2], acc[i][b + 3]);
 #pragma unroll
         for (int b = 0; b < FN; b += W) {
           u32x4_t part[2];
