@@ -1,6 +1,6 @@
 // 4-bit matrices (format: mx4.hpp): pack, of a matrix or of its transpose, and unpack
-// (gfx950). Bound by memory: 16384 x 4096 bf16 packed in 33 us and unpacked in 29,
-// 5.1 and 5.9 TB/s.
+// (gfx950). Bound by memory: 16384 x 4096 bf16 packed in 31 us and unpacked in 29,
+// 5.4 and 5.9 TB/s.
 #include "mx4.hpp"
 #include "train_ops.hpp"
 
@@ -10,7 +10,7 @@ namespace ma {
 // values per lane, 4 lanes a block of 32. A block of threads takes 16 rows and up to 4 k-tiles of
 // each, all in flight: 1 KB of a row of bf16 and, for each k-tile, 64 bytes of scales at once
 // (of narrower matrices, more rows). Along the rows, one k-tile after the other, with scales stored as
-// bytes: 35 us, now 33.
+// bytes: 35 us for 16384 x 4096 bf16, so 33 (both with loads through the caches).
 constexpr int kMx4Unroll = 4;
 
 struct Mx4Place {
@@ -175,7 +175,9 @@ hipError_t launch_mx4_pack(const Mx4Args& a, int x_dt, bool transpose, hipStream
     else hipLaunchKernelGGL(k_mx4_pack_t<DT_BF16>, grid, dim3(64), 0, s, a);
     return hipGetLastError();
   }
-  const bool stream = a.rows * a.cols * (f32 ? 4 : 2) > kStreamBytes;
+  // x past the caches from half of what they keep (16384 x 4096 bf16 30 us against 33; 8192 x 2048,
+  // written just before, 21.6 with its writer against 20.6)
+  const bool stream = a.rows * a.cols * (f32 ? 4 : 2) > kStreamBytes / 2;
   auto go = [&](auto k) { hipLaunchKernelGGL(k, mx4_grid(a), dim3(256), 0, s, a, mx4_log2t(mx4_tiles(a.cols))); };
   if (f32) stream ? go(k_mx4_pack<DT_F32, true>) : go(k_mx4_pack<DT_F32, false>);
   else stream ? go(k_mx4_pack<DT_BF16, true>) : go(k_mx4_pack<DT_BF16, false>);

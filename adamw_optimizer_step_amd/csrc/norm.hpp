@@ -49,8 +49,8 @@ template <int DT, int G, bool QUADS> struct Chunk {
   Raw8<DT> r = raw_zero<DT>();
   static constexpr int H = 1, E = 8;   // parts of E values
   static __device__ __forceinline__ int col(int c, int, int t) { return (c * G + t) * 8; }
-  __device__ __forceinline__ void load(const unsigned char* row, int c, int t, int cols) {
-    if (col(c, 0, t) < cols) r = raw_load_row<DT>(row, col(c, 0, t), cols);
+  template <bool NT = false> __device__ __forceinline__ void load(const unsigned char* row, int c, int t, int cols) {
+    if (col(c, 0, t) < cols) r = raw_load_row<DT, NT>(row, col(c, 0, t), cols);
   }
   __device__ __forceinline__ void f32(int c, int, int t, int cols, float (&v)[8]) const { raw_f32_row<DT>(r, col(c, 0, t), cols, v); }
   template <bool NT> static __device__ __forceinline__ void store(unsigned char* row, int col, int cols, const float (&v)[8]) { store_row<DT, NT>(row, col, cols, v); }
@@ -59,10 +59,10 @@ template <int DT, int G> struct Chunk<DT, G, true> {
   Raw4<DT> r[2] = {quad_zero<DT>(), quad_zero<DT>()};
   static constexpr int H = 2, E = 4;
   static __device__ __forceinline__ int col(int c, int h, int t) { return (c * 2 + h) * G * 4 + t * 4; }
-  __device__ __forceinline__ void load(const unsigned char* row, int c, int t, int cols) {
+  template <bool NT = false> __device__ __forceinline__ void load(const unsigned char* row, int c, int t, int cols) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (col(c, h, t) < cols) r[h] = quad_load_row<DT>(row, col(c, h, t), cols);
+      if (col(c, h, t) < cols) r[h] = quad_load_row<DT, NT>(row, col(c, h, t), cols);
   }
   __device__ __forceinline__ void f32(int c, int h, int t, int cols, float (&v)[4]) const { quad_f32<DT>(r[h], col(c, h, t), cols, v); }
   template <bool NT> static __device__ __forceinline__ void store(unsigned char* row, int col, int cols, const float (&v)[4]) { quad_store_row<DT, NT>(row, col, cols, v); }

@@ -11,9 +11,9 @@
 // One read of every operand: a group of G lanes holds a row in registers (norm.hpp).
 // Sums are fp32, in a fixed order; each output is rounded once.
 //
-// Bound by memory. With a bf16 residual to 8 bits, 24576 x 2048: 65 us, 5.4 TB/s; onto a
+// Bound by memory. With a bf16 residual to 8 bits, 24576 x 2048: 58.5 us, 6.1 TB/s; onto a
 // fp32 stream, 1537 x 2047: 8.9 (4.2, one wave of blocks); backward with dtotal, 49152 x 1024
-// bf16: 75.6 (5.3) and 4.6 for the column sums; 1 x 1024: 2.2, a chain of a load, a reduction
+// bf16: 70.6 (5.7) and 4.7 for the column sums; 1 x 1024: 2.2, a chain of a load, a reduction
 // and a store.
 #include "norm.hpp"
 
@@ -32,6 +32,9 @@ __device__ __forceinline__ void round_to(float (&v)[E]) {
   }
 }
 
+// NT: more bytes than the caches keep, none of which is read or written twice: loads and stores
+// non-temporal (24576 x 2048 to 8 bits 59 us; loads through the caches 66, stores 68; 16384 x 4096 onto
+// a fp32 stream 115, 133, 136).
 template <int XD, int TD, int YD, int G, int CH, bool NT>
 __global__ void __launch_bounds__(norm_threads(G), 4) k_rms_fwd(const RmsFwdArgs a) {
   constexpr int ROWS = norm_threads(G) / G;
@@ -55,8 +58,8 @@ __global__ void __launch_bounds__(norm_threads(G), 4) k_rms_fwd(const RmsFwdArgs
       next[c] = XC();
       beside[c] = RC();
       if (r >= a.rows) continue;
-      next[c].load(elem_ptr<XD>(a.x, r * a.cols), c, t, a.cols);
-      if (a.residual) beside[c].load(elem_ptr<TD>(a.residual, r * a.cols), c, t, a.cols);
+      next[c].template load<NT>(elem_ptr<XD>(a.x, r * a.cols), c, t, a.cols);
+      if (a.residual) beside[c].template load<NT>(elem_ptr<TD>(a.residual, r * a.cols), c, t, a.cols);
     }
   };
   if constexpr (AHEAD) load(row);
@@ -197,8 +200,9 @@ __global__ void __launch_bounds__(norm_bwd_threads(G)) k_rms_bwd(const RmsBwdArg
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[c][e] = 0.0f;
-  // a row's operands, loaded while the row before it is computed; x comes from a
-  // forward pass long ago and is not read again soon (non-temporal), dy and dtotal are fresh
+  // a row's operands, loaded while the row before it is computed; x and dtotal are read here
+  // for the last time, non-temporal (x 85.9 -> 77.8 us for 49152 x 1024, dtotal 28.3 -> 26.2 for
+  // 16384 x 1024). dy not: wide rows read it twice (2000 x 16384 76 us, else 84)
   constexpr int XR = raw_dt<XD>();
   struct Row {
     Raw8<XR> x[CH];
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(G)) k_rms_bwd(const RmsBwdArg
         r.x[c] = raw_load_row<XR, true>(elem_ptr<XR>(a.x, row * a.cols), col, a.cols);
       }
       r.dy[c] = raw_load_row<DYD>(elem_ptr<DYD>(a.dy, row * a.cols), col, a.cols);
-      if (a.dtotal) r.dt[c] = raw_load_row<DXD>(elem_ptr<DXD>(a.dtotal, row * a.cols), col, a.cols);
+      if (a.dtotal) r.dt[c] = raw_load_row<DXD, true>(elem_ptr<DXD>(a.dtotal, row * a.cols), col, a.cols);
     }
     return r;
   };
@@ -344,7 +348,9 @@ static hipError_t rms_fwd(const RmsFwdArgs& a, hipStream_t s) {
     const int64_t per = norm_threads(G) / G, want = (a.rows + per - 1) / per, most = (int64_t)256 * kNormWaves * 64 / norm_threads(G);
     const dim3 grid((unsigned)(want < most ? want : most)), block(norm_threads(G));
     const int64_t bytes = a.rows * a.cols * (elem_bytes<XD>() + (a.residual ? 2 * elem_bytes<TD>() : 0) + (a.y ? elem_bytes<YD>() : 0) + (a.q ? 1 : 0));
-    if (bytes > kStreamBytes) hipLaunchKernelGGL((k_rms_fwd<XD, TD, YD, G, CH, true>), grid, block, 0, s, a);
+    // (half: 8192 x 2048 to 8 bits, 117 MB, 22 us against 25, and 40 against 43 with its neighbours;
+    // 4096 x 2048 with what reads its results 32 against 30)
+    if (bytes > kStreamBytes / 2) hipLaunchKernelGGL((k_rms_fwd<XD, TD, YD, G, CH, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((k_rms_fwd<XD, TD, YD, G, CH, false>), grid, block, 0, s, a);
     return hipGetLastError();
   };

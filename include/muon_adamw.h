@@ -405,7 +405,7 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
 
 /* Root-mean-square norm with the residual's addition, per row (rows <= 2^24,
  * cols <= 16384, rows * cols <= 2^36):
- *   t = x + residual, rounded to the residual's type, written to `total`;
+ *   t = x + residual, added in fp32 and rounded to the residual's type, written to `total`;
  *       without a residual t = x, and `total` must be null
  *   rstd = 1 / sqrt(sum t^2 / cols + eps)
  *   y = t * rstd * gain                        gain: cols fp32 values, may be null
@@ -474,7 +474,7 @@ int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const
  *          the lower half; zero beyond cols
  *   scale  P/MA_MX4_TILE x rows x 4 bytes, 4-byte aligned: for every tile of columns
  *          and row the bytes of its 4 blocks; the byte s stands for 2^(s - 127), 255
- *          for NaN (E8M0)
+ *          for NaN (E8M0), also in a block beyond cols, where packing writes 1
  * Packing takes the least exponent e in -126..125 for which the block's largest
  * magnitude over 2^e rounds to at most 6, and rounds x / 2^e to nearest even: every
  * value is off by half a step at most (|x| / 5 from 2^e up, 2^e / 4 below). At
