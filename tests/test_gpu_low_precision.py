@@ -466,6 +466,25 @@ def test_product_of_8_bit_rows_keeps_small_products_beside_large_ones(rows, outs
     assert bool(((got - want).abs() <= cut * (1 + half(BF16)) + half(BF16) * want.abs()).all())
 
 
+@pytest.mark.parametrize("rows,outs", [(256, 256), (20, 256), (700, 900)])
+@pytest.mark.parametrize("yd", [BF16, F32])
+def test_product_takes_every_8_bit_value(rows, outs, yd):
+    """Row r holds the byte r % 256 in column r % 256, and w is the identity; a NaN reaches its whole row."""
+    say("mx4_matmul, every byte", rows, outs, yd)
+    r = torch.arange(rows, device=DEV)
+    q = torch.zeros(rows, 256, dtype=torch.uint8, device=DEV)
+    q[r, r % 256] = (r % 256).to(torch.uint8)
+    x = ma.ActCheckpoint(q, torch.full((rows, 2), 127 + 3, dtype=torch.uint8, device=DEV), 256)
+    w = ma.mx4_pack(torch.eye(outs, 256, device=DEV))
+    value = torch.arange(256, device=DEV).to(torch.uint8).view(torch.float8_e4m3fn).float() * 8
+    want = torch.zeros(rows, outs, device=DEV)
+    want[r, r % 256] = value[r % 256]
+    want[torch.isnan(value[r % 256])] = float("nan")
+    got = ma.mx4_matmul(x, w, dtype=yd)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.float()), torch.nan_to_num(want))
+
+
 def test_product_shapes_and_defaults():
     x, w = ma.mx4_pack(rand((4, 40), 190)), ma.mx4_pack(rand((6, 40), 191))
     y = ma.mx4_matmul(x, w)
