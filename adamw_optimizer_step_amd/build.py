@@ -14,6 +14,8 @@ import re
 import subprocess
 import sys
 
+from . import wait_states
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
@@ -100,6 +102,9 @@ def _compile(src: str):
         raise RuntimeError(f"hipcc failed for {src}:\n{err}")
     if err.strip():
         print(err, file=sys.stderr)
+    bad = wait_states.violations(wait_states.disassemble(obj))
+    if bad:
+        raise RuntimeError(f"{src}: wait states are missing:\n  " + "\n  ".join(bad))
     return obj, res
 
 

@@ -141,7 +141,9 @@ typedef __attribute__((address_space(3))) unsigned char lds_u8_t;
 
 // 16 bytes per lane from memory, at base + off, into LDS, the lanes' side by side from `to` (base
 // and `to` the same for every lane). In assembler, as the compiler waits for all LDS reads at
-// each one's use where it knows of such a copy under way. Nothing is loaded into a register.
+// each one's use where it knows of such a copy under way. Nothing is loaded into a register. A copy
+// comes one wait state after m0 was written (wait_states.py checks that, and the others below). m0 is
+// reserved: the compiler keeps nothing in it, and cannot be told of it.
 __device__ __forceinline__ void copy_chunks(const uint8_t* base, uint32_t off, lds_u8_t* to) {
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)to);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(at), "v"(off), "s"(base) : "memory");
@@ -187,9 +189,10 @@ __device__ __forceinline__ void block_barrier() {
 }
 
 // acc += w x, 16 x 16 outputs and 128 k, in place: from the builtin the compiler makes a new
-// accumulator each time, and moves them all. FRESH: w, x or a scale may have been computed by
-// the instruction before, which needs two wait states. Whoever reads acc otherwise calls
-// settled() first.
+// accumulator each time, and moves them all. What a vector instruction wrote is read two wait states
+// later at the earliest, which the compiler does not see to here. FRESH: w, x or a scale may
+// have been computed by the instruction before. acc: cleared() has the wait. Whoever reads acc
+// otherwise calls settled() first.
 template <int XB> struct MxRow { typedef u32x4_t T; };   // a lane's 32 values of x
 template <> struct MxRow<8> { typedef i32x8_t T; };
 template <int XB, bool FRESH>
@@ -210,6 +213,15 @@ __device__ __forceinline__ void mx_mfma16_into(f32x4_t& acc, u32x4_t w, typename
 __device__ __forceinline__ void settled(f32x4_t& a, f32x4_t& b, f32x4_t& c, f32x4_t& d) {
 #if defined(__HIP_DEVICE_COMPILE__)
   asm volatile("s_nop 15\n\ts_nop 7" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+#endif
+}
+
+// Zeros in these 4 accumulators, and two wait states. They are written here: plain zeros the compiler
+// writes again right in front of the MFMA that reads them first.
+__device__ __forceinline__ void cleared(f32x4_t& a, f32x4_t& b, f32x4_t& c, f32x4_t& d) {
+  a = b = c = d = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 1" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
 #endif
 }
 
@@ -375,10 +387,13 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
   };
 
   f32x4_t acc[FM][FN];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int b = 0; b < FN; b += 4) cleared(acc[i][b], acc[i][b + 1], acc[i][b + 2], acc[i][b + 3]);
+  };
+  clear();
 
   // fragments: lane (l16, g) holds row l16 of each block and 32 values from 32 g (8 bits: two
   // times 16, from 16 g and 64 further), and their scale
@@ -559,8 +574,6 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
           }
           if constexpr (ADD && i + 1 < FM) load(i + 1, b);
         }
-#pragma unroll
-        for (int b = 0; b < FN; ++b) acc[i][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         __builtin_amdgcn_sched_barrier(0);
       });
     };
@@ -575,6 +588,7 @@ __global__ void __launch_bounds__(TL::NT, TL::NW * TL::BLOCKS / 4) k_mx4_tile(co
       else if (a.stream) put(Y(), No(), Yes());
       else put(Y(), No(), No());
     }
+    clear();
   };
 
   copies_of(job_at(job));
