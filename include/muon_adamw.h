@@ -493,11 +493,8 @@ int ma_mx4_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t 
 /* A linear layer on held values: y[m,n] (+)= sum over k of x[m,k] * w[n,k].
  * wq, wscale: a 4-bit outs x ins matrix; xq, xscale: rows x ins held in 4 bits
  * (x_bits 4) or as an 8-bit checkpoint (x_bits 8). The held values are multiplied as
- * they are; sums are fp32, y (rows x outs) is rounded once. Only with 8-bit rows and a
- * bf16 y, of 8 consecutive k the products lose what is below 2^-13 of the largest one's
- * power of two (2e-5 of ordinary results, whose rounding is 2e-3; an fp32 y loses
- * nothing, and takes twice the instructions). A NaN that is held reaches every output of its row (of
- * w: of its column).
+ * they are and summed in fp32, and y (rows x outs) is rounded once. A NaN that is held
+ * reaches every output of its row (of w: of its column).
  * Limits: rows <= 2^24, outs, ins <= 2^23, rows * outs, rows * P and outs * P <= 2^36
  * (P = ins rounded up to a multiple of MA_MX4_TILE). workspace: at least ma_mx4_matmul_workspace_size
  * bytes, which may be 0; that is the need of exactly these sizes. */
