@@ -175,22 +175,22 @@ hipError_t launch_mx4_pack(const Mx4Args& a, int x_dt, bool transpose, hipStream
     else hipLaunchKernelGGL(k_mx4_pack_t<DT_BF16>, grid, dim3(64), 0, s, a);
     return hipGetLastError();
   }
-  // x past the caches from half of what they keep (16384 x 4096 bf16 30 us against 33; 8192 x 2048,
-  // written just before, 21.6 with its writer against 20.6)
-  const bool stream = a.rows * a.cols * (f32 ? 4 : 2) > kStreamBytes / 2;
+  // bf16 x past the caches from half of what they keep (16384 x 4096 30 us against 33; 8192 x 2048,
+  // written just before, 21.6 with its writer against 20.6); fp32 by 8 columns always through them (rows.hpp)
+  const bool stream = a.rows * a.cols * 2 > kStreamBytes / 2;
   auto go = [&](auto k) { hipLaunchKernelGGL(k, mx4_grid(a), dim3(256), 0, s, a, mx4_log2t(mx4_tiles(a.cols))); };
-  if (f32) stream ? go(k_mx4_pack<DT_F32, true>) : go(k_mx4_pack<DT_F32, false>);
+  if (f32) go(k_mx4_pack<DT_F32, false>);
   else stream ? go(k_mx4_pack<DT_BF16, true>) : go(k_mx4_pack<DT_BF16, false>);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_unpack(const Mx4Args& a, int out_dt, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
-  const bool stream = a.rows * a.cols * (out_dt == DT_F32 ? 4 : 2) > kStreamBytes;
+  const bool stream = a.rows * a.cols * 2 > kStreamBytes;   // (bf16 only, as in packing)
   const int64_t per = 16 * kMx4Unroll;
   const dim3 grid((unsigned)((a.rows * mx4_tiles(a.cols) + per - 1) / per));
   auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a); };
-  if (out_dt == DT_F32) stream ? go(k_mx4_unpack<DT_F32, true>) : go(k_mx4_unpack<DT_F32, false>);
+  if (out_dt == DT_F32) go(k_mx4_unpack<DT_F32, false>);
   else stream ? go(k_mx4_unpack<DT_BF16, true>) : go(k_mx4_unpack<DT_BF16, false>);
   return hipGetLastError();
 }

@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(G)) k_rms_bwd(const RmsBwdArg
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[c][e] = 0.0f;
   // a row's operands, loaded while the row before it is computed; x and dtotal are read here
-  // for the last time, non-temporal (x 85.9 -> 77.8 us for 49152 x 1024, dtotal 28.3 -> 26.2 for
-  // 16384 x 1024). dy not: wide rows read it twice (2000 x 16384 76 us, else 84)
+  // for the last time, non-temporal where they are bf16 (x 85.9 -> 77.8 us for 49152 x 1024, dtotal 28.3 -> 26.2
+  // for 16384 x 1024). dy not: wide rows read it twice (2000 x 16384 76 us, else 84)
   constexpr int XR = raw_dt<XD>();
   struct Row {
     Raw8<XR> x[CH];
