@@ -296,8 +296,8 @@ struct Mx4Job {
 // and its first fragments read, before the results are stored, and the stores end while it is
 // worked on. Results go from the registers to memory, without LDS or a barrier.
 //
-// Measured: 12288 x (16384 x 4096) of 4 bits 447 us, 3.7 PFLOP/s, the matrix units busy for 44 % of the
-// cycles at 2.0 GHz; 12288 x (4096 x 16384) of 8 bits 1150, 1.4, 59 % at 1.9 GHz. A k-tile of 256 x 256 takes 0.9 us
+// Measured, call after call: 12288 x (16384 x 4096) of 4 bits 423 to 437 us, 3.8 PFLOP/s, the matrix units busy for 44 %
+// of the cycles at 1.9 GHz; 12288 x (4096 x 16384) of 8 bits 1150, 1.4, 59 % at 1.9 GHz. A k-tile of 256 x 256 takes 0.9 us
 // (4 bits; 2.9 of 8), of which the MFMAs alone are 0.61, the LDS reads alone 0.78, the copies alone 0.77; the
 // stores at a tile's end 5 us (bf16) to 15 (fp32), with all blocks' at the same time. Tried, and no faster: blocks
 // started at different times (+1 to +8 %), 4 waves of 128 x 128 (spills), 32 x 32 x 64 instructions,
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(256) k_mx4_join(const Mx4MatmulArgs a) {
 }
 
 // Few rows: blocks of 16, 32 or 64 rows, and waves per block: 8 of them, fewer where blocks * waves would be
-// beyond 32 per CU or a wave would have less than 2 k-tiles. (1 x (4096 x 4096) of 4 bits 4.5 us with 8 waves,
+// beyond 32 per CU or a wave would have less than 2 k-tiles. (All of 4 bits: 1 x (4096 x 4096) 4.5 us with 8 waves,
 // 4.8 with 16; 1 x (4096 x 16384) 8.8 and 9.6; 1 x (16384 x 4096) 8.7 with 8 and 9.0 with 4.)
 static int mx4_rows_mb(int64_t rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
 static int64_t mx4_rows_blocks(int64_t rows, int64_t outs) {

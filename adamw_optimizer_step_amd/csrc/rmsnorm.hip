@@ -11,9 +11,9 @@
 // One read of every operand: a group of G lanes holds a row in registers (norm.hpp).
 // Sums are fp32, in a fixed order; each output is rounded once.
 //
-// Bound by memory. With a bf16 residual to 8 bits, 24576 x 2048: 58.5 us, 6.1 TB/s; onto a
-// fp32 stream, 1537 x 2047: 8.9 (4.2, one wave of blocks); backward with dtotal, 49152 x 1024
-// bf16: 70.6 (5.7) and 4.7 for the column sums; 1 x 1024: 2.2, a chain of a load, a reduction
+// Bound by memory. With a bf16 residual to 8 bits, 24576 x 2048: 58.8 us, 6.0 TB/s; onto a
+// fp32 stream, 1537 x 2047: 8.6 (4.4; 513 of 1024 blocks take two rows); backward with dtotal, 49152 x 1024
+// bf16: 71 (5.7) and 4.6 for the column sums; 1 x 1024: 2.2, a chain of a load, a reduction
 // and a store.
 #include "norm.hpp"
 

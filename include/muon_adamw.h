@@ -413,7 +413,8 @@ int ma_layernorm_backward(const void* dy, int32_t dy_dtype, const void* x, int32
  * pass reads. y may be null where held_q and held_scale (both or neither) are
  * given: they receive y as an 8-bit checkpoint (ma_act_pack), rounded from fp32
  * once; with y given too, both are written. Sums are fp32: a row whose sum of
- * squares passes its range has rstd 0; a row of zeros with eps 0 has y NaN. */
+ * squares passes its range has rstd 0. With eps 0 a row of zeros has y NaN, one whose
+ * squares all vanish in fp32 rstd infinite, and squares below 2^-126 lose bits. */
 int ma_rmsnorm_forward(const void* x, int32_t x_dtype, const void* residual, int32_t residual_dtype, int64_t rows, int64_t cols,
                        const float* gain, float eps, void* total, void* y, int32_t y_dtype, float* rstd, uint8_t* held_q,
                        uint8_t* held_scale, void* stream);
@@ -481,8 +482,9 @@ int ma_act_weight_grad(const void* dy, int32_t dy_dtype, const uint8_t* q, const
  * e = 125 values stop at 6 * 2^125. A block with a NaN or an infinity is held as NaN.
  * Every held value is exact in bf16. transpose = 1 packs x^T: q and scale then
  * describe a cols x rows matrix, whose blocks go along x's rows. Unpacking rounds
- * nothing, whatever the scale bytes. Limits: rows, cols <= 2^24, and padded rows of
- * at most 2^36 values in all (2^35 where x or out is fp32). */
+ * nothing; under the scale bytes 253 and 254, which packing does not write, values from
+ * 4 and from 2 are beyond either type and come out infinite. Limits: rows, cols <=
+ * 2^24, and padded rows of at most 2^36 values in all (2^35 where x or out is fp32). */
 #define MA_MX4_BLOCK 32
 #define MA_MX4_TILE 128
 int ma_mx4_pack(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int32_t transpose, uint8_t* q, uint8_t* scale,
